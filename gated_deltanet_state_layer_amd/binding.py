@@ -28,6 +28,9 @@ GDN_BF16 = 1
 GDN_VALIDATE = 1
 GDN_GROUP_KERNEL = 2
 GDN_STATIC_SCRATCH_BYTES = 64 << 20
+GDN_BLOCK_NORM_MAX_HIDDEN = 16384
+GDN_MX_GROUP = 32
+GDN_MX_MAX_IN = 1048576
 
 EXPORTED = (
     "gdn_pool_bytes", "gdn_pool_create", "gdn_pool_destroy", "gdn_slot_reset",
@@ -35,7 +38,9 @@ EXPORTED = (
     "gdn_prefill_chunked", "gdn_prefill_chunked_static", "gdn_prefill_chunked_ckpt",
     "gdn_slot_copy", "gdn_ring_verify",
     "gdn_ring_commit", "gdn_ring_flush", "gdn_in_proj_workspace_bytes", "gdn_in_proj",
-    "gdn_pool_error", "gdn_status_string",
+    "gdn_pool_error", "gdn_status_string", "gdn_block_norm", "gdn_gated_norm",
+    "gdn_mx_quantize", "gdn_mx_dequantize", "gdn_mx_proj_workspace_bytes", "gdn_mx_proj",
+    "gdn_mx_in_proj_workspace_bytes", "gdn_mx_in_proj",
 )
 
 
@@ -69,6 +74,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                            "`python -m gated_deltanet_state_layer_amd.build`")
     lib = ctypes.CDLL(path)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    F32 = ctypes.c_float
     PSZ = ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "gdn_pool_bytes": [ctypes.POINTER(PoolDesc), PSZ, PSZ],
@@ -89,6 +95,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "gdn_in_proj_workspace_bytes": [P, I64, I32, PSZ],
         "gdn_in_proj": [P, I64, I32, P, P, P, P, P, P, P, P, SZ, P],
         "gdn_pool_error": [P, P, ctypes.POINTER(I32)],
+        "gdn_block_norm": [I64, I32, I32, I32, P, I64, P, F32, P, I64, P, I64, P, F32, F32, P, I64,
+                           P],
+        "gdn_gated_norm": [P, I64, P, I64, P, I64, P, F32, I32, P, I64, P],
+        "gdn_mx_quantize": [I64, I32, I32, P, P, P, P],
+        "gdn_mx_dequantize": [I64, I32, P, P, I32, P, P],
+        "gdn_mx_proj_workspace_bytes": [I64, I32, I32, PSZ],
+        "gdn_mx_proj": [I64, I32, I32, P, I64, P, P, I32, P, I64, P, SZ, P],
+        "gdn_mx_in_proj_workspace_bytes": [P, I64, I32, I32, PSZ],
+        "gdn_mx_in_proj": [P, I64, I32, P, P, P, P, P, P, P, P, P, P, SZ, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -173,6 +188,118 @@ def pool_bytes(desc: PoolDesc):
     _check(lib.gdn_pool_bytes(ctypes.byref(desc), ctypes.byref(sb), ctypes.byref(ab)),
            "gdn_pool_bytes")
     return sb.value, ab.value
+
+
+_DTYPES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+
+
+def _dtype(t, name):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected bfloat16 or float32")
+    return code
+
+
+def _rows(t, name, shape, dtype):
+    """Host-side check of a device tensor of this shape and dtype whose rows
+    (everything behind the first dimension) are contiguous; returns the
+    elements between rows."""
+    if t is None:
+        raise ValueError(f"{name}: missing")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: not a device tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return t.numel() // shape[0] if shape[0] else 0
+    if shape[0] and not t[0].is_contiguous():
+        raise ValueError(f"{name}: rows are not contiguous")
+    return t.stride(0)
+
+
+def block_norm(residual, w, out, y=None, w_post=None, residual_out=None, res_scale=1.0,
+               w_offset=0.0, eps=1e-6, stream=None):
+    """gdn_block_norm: with a block's output y, residual_out = residual +
+    res_scale * y (y normalised with w_post first, if given), and out = the
+    norm of that sum times (w_offset + w).  Without y, the norm of residual.
+    residual and residual_out share one dtype, y and out another."""
+    lib = load_library()
+    if residual.dim() != 2:
+        raise ValueError(f"residual: shape {tuple(residual.shape)}, expected [tokens, hidden]")
+    shape = n, hidden = residual.shape
+    rdt, iodt = _dtype(residual, "residual"), _dtype(out, "out")
+    ld_r = _rows(residual, "residual", shape, residual.dtype)
+    ld_x = _rows(out, "out", shape, out.dtype)
+    _need(w, "w", hidden, torch.float32)
+    ld_y = ld_ro = 0
+    if y is not None:
+        ld_y = _rows(y, "y", shape, out.dtype)
+        ld_ro = _rows(residual_out, "residual_out", shape, residual.dtype)
+        if w_post is not None:
+            _need(w_post, "w_post", hidden, torch.float32)
+    elif w_post is not None or residual_out is not None:
+        raise ValueError("w_post and residual_out need y")
+    _check(lib.gdn_block_norm(n, hidden, iodt, rdt, _ptr(y), ld_y, _ptr(w_post), res_scale,
+                              _ptr(residual), ld_r, _ptr(residual_out), ld_ro, _ptr(w), w_offset,
+                              eps, _ptr(out), ld_x, _stream(stream)), "gdn_block_norm")
+    return out
+
+
+def mx_quantize(src, codes, scales, stream=None):
+    """gdn_mx_quantize: src [rows, cols] (bfloat16 or float32) to 4-bit codes
+    [rows, cols/2] and scale bytes [rows, cols/32] (both uint8)."""
+    lib = load_library()
+    rows, cols = src.shape
+    code = _dtype(src, "src")
+    _need(src, "src", rows * cols, src.dtype)
+    _need(codes, "codes", rows * cols // 2, torch.uint8)
+    _need(scales, "scales", rows * cols // GDN_MX_GROUP, torch.uint8)
+    _check(lib.gdn_mx_quantize(rows, cols, code, _ptr(src), _ptr(codes), _ptr(scales),
+                               _stream(stream)), "gdn_mx_quantize")
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, out, stream=None):
+    """gdn_mx_dequantize: the weights [rows, cols] (bfloat16 or float32) that
+    codes and scales stand for."""
+    lib = load_library()
+    rows, cols = out.shape
+    code = _dtype(out, "out")
+    _need(out, "out", rows * cols, out.dtype)
+    _need(codes, "codes", rows * cols // 2, torch.uint8)
+    _need(scales, "scales", rows * cols // GDN_MX_GROUP, torch.uint8)
+    _check(lib.gdn_mx_dequantize(rows, cols, _ptr(codes), _ptr(scales), code, _ptr(out),
+                                 _stream(stream)), "gdn_mx_dequantize")
+    return out
+
+
+def mx_proj_workspace_bytes(n_tok, n_in, n_out):
+    lib = load_library()
+    n = ctypes.c_size_t()
+    _check(lib.gdn_mx_proj_workspace_bytes(n_tok, n_in, n_out, ctypes.byref(n)),
+           "gdn_mx_proj_workspace_bytes")
+    return n.value
+
+
+def mx_proj(x, codes, scales, out, workspace=None, stream=None):
+    """gdn_mx_proj: out [tokens, n_out] (bfloat16 or float32) = x [tokens,
+    n_in] (bfloat16) times the transposed 4-bit weights."""
+    lib = load_library()
+    if x.dim() != 2 or out.dim() != 2:
+        raise ValueError("x and out: expected [tokens, channels]")
+    (n_tok, n_in), n_out = x.shape, out.shape[1]
+    ld_x = _rows(x, "x", (n_tok, n_in), torch.bfloat16)
+    ld_y = _rows(out, "out", (n_tok, n_out), out.dtype)
+    code = _dtype(out, "out")
+    _need(codes, "codes", n_out * n_in // 2, torch.uint8)
+    _need(scales, "scales", n_out * n_in // GDN_MX_GROUP, torch.uint8)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.gdn_mx_proj(n_tok, n_in, n_out, _ptr(x), ld_x, _ptr(codes), _ptr(scales), code,
+                           _ptr(out), ld_y, _ptr(workspace), ws_bytes, _stream(stream)),
+           "gdn_mx_proj")
+    return out
 
 
 class Pool:
@@ -377,6 +504,52 @@ class Pool:
                                             _ptr(workspace), ws_bytes, _stream(stream)),
                "gdn_prefill_chunked_ckpt")
         return out
+
+    def gated_norm(self, o, z, w, out, eps=1e-6, stream=None):
+        """gdn_gated_norm: out [tokens, h_v, d_v] = the per-head norm of o times
+        w times z * sigmoid(z).  out may be bfloat16 or float32."""
+        lib = load_library()
+        d = self.desc
+        shape = (o.shape[0], d.h_v, d.d_v)
+        ld_o = _rows(o, "o", shape, self.io_torch)
+        ld_z = _rows(z, "z", shape, self.io_torch)
+        ld_out = _rows(out, "out", shape, out.dtype)
+        code = _dtype(out, "out")
+        _need(w, "w", d.d_v, torch.float32)
+        _check(lib.gdn_gated_norm(self._h, shape[0], _ptr(o), ld_o, _ptr(z), ld_z, _ptr(w), eps,
+                                  code, _ptr(out), ld_out, _stream(stream)), "gdn_gated_norm")
+        return out
+
+    def mx_in_proj_workspace_bytes(self, n_tok, hidden, with_z=True):
+        lib = load_library()
+        n = ctypes.c_size_t()
+        _check(lib.gdn_mx_in_proj_workspace_bytes(self._h, n_tok, hidden, int(with_z),
+                                                  ctypes.byref(n)),
+               "gdn_mx_in_proj_workspace_bytes")
+        return n.value
+
+    def mx_in_proj(self, x, codes, scales, q, k, v, a, b, z=None, workspace=None, stream=None):
+        """gdn_mx_in_proj: x [n_tok, hidden] bf16 times the 4-bit weights whose
+        rows are q | k | v | z | a | b (no z rows without z), into the raw
+        q, k, v, the gate z and the activated gates a, b."""
+        lib = load_library()
+        n_tok, hidden = int(x.shape[0]), int(x.shape[1])
+        d = self.desc
+        n_out = self.c_conv + (0 if z is None else d.h_v * d.d_v) + 2 * d.h_v
+        _need(x, "x", n_tok * hidden, torch.bfloat16)
+        _need(codes, "codes", n_out * hidden // 2, torch.uint8)
+        _need(scales, "scales", n_out * hidden // GDN_MX_GROUP, torch.uint8)
+        _need(q, "q", n_tok * d.h_k * d.d_k, self.io_torch)
+        _need(k, "k", n_tok * d.h_k * d.d_k, self.io_torch)
+        _need(v, "v", n_tok * d.h_v * d.d_v, self.io_torch)
+        if z is not None:
+            _need(z, "z", n_tok * d.h_v * d.d_v, self.io_torch)
+        _need(a, "a", n_tok * d.h_v, torch.float32)
+        _need(b, "b", n_tok * d.h_v, torch.float32)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib.gdn_mx_in_proj(self._h, n_tok, hidden, _ptr(x), _ptr(codes), _ptr(scales),
+                                  _ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(a), _ptr(b),
+                                  _ptr(workspace), ws_bytes, _stream(stream)), "gdn_mx_in_proj")
 
     def _prefill_args(self, n_seq, cu_seqlens, slot_ids, total_tokens, q, k, v, a, b, conv_w,
                       out):

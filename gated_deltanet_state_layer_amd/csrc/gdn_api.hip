@@ -532,6 +532,162 @@ gdn_status gdn_in_proj(gdn_pool* pool, int64_t n_tok, int32_t hidden, const void
                : GDN_ERR_HIP;
 }
 
+static bool dtype_ok(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
+static size_t elem_bytes(gdn_dtype t) { return t == GDN_BF16 ? 2 : 4; }
+
+gdn_status gdn_block_norm(int64_t n_tok, int32_t hidden, gdn_dtype io_dtype, gdn_dtype res_dtype,
+                          const void* y, int64_t ld_y, const float* w_post, float res_scale,
+                          const void* res, int64_t ld_res, void* res_out, int64_t ld_res_out,
+                          const float* w_pre, float w_offset, float eps, void* x, int64_t ld_x,
+                          void* stream) {
+    if (n_tok < 0 || hidden < 1 || !dtype_ok(io_dtype) || !dtype_ok(res_dtype)) return GDN_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(res_scale) || !std::isfinite(w_offset))
+        return GDN_ERR_INVALID_ARG;
+    if (hidden > GDN_BLOCK_NORM_MAX_HIDDEN) return GDN_ERR_UNSUPPORTED;
+    if (n_tok == 0) return GDN_OK;
+    if (!res || !w_pre || !x) return GDN_ERR_INVALID_ARG;
+    if (y ? !res_out : (res_out || w_post)) return GDN_ERR_INVALID_ARG;
+    if (n_tok > 1 && (ld_res < hidden || ld_x < hidden || (y && (ld_y < hidden || ld_res_out < hidden))))
+        return GDN_ERR_INVALID_ARG;
+    const size_t io = elem_bytes(io_dtype), rs = elem_bytes(res_dtype);
+    if (!aligned(y, io) || !aligned(x, io) || !aligned(res, rs) || !aligned(res_out, rs) ||
+        !aligned(w_pre, 4) || !aligned(w_post, 4))
+        return GDN_ERR_INVALID_ARG;
+    return launch_block_norm(n_tok, hidden, io_dtype, res_dtype, y, ld_y, w_post, res_scale, res, ld_res,
+                             res_out, ld_res_out, w_pre, w_offset, eps, x, ld_x,
+                             as_stream(stream)) == hipSuccess
+               ? GDN_OK
+               : GDN_ERR_HIP;
+}
+
+gdn_status gdn_gated_norm(const gdn_pool* pool, int64_t n_tok, const void* o, int64_t ld_o, const void* z,
+                          int64_t ld_z, const float* w, float eps, gdn_dtype out_dtype, void* out,
+                          int64_t ld_out, void* stream) {
+    if (!pool || n_tok < 0 || !dtype_ok(out_dtype) || !(eps >= 0.f) || !std::isfinite(eps))
+        return GDN_ERR_INVALID_ARG;
+    if (n_tok == 0) return GDN_OK;
+    if (!o || !z || !w || !out) return GDN_ERR_INVALID_ARG;
+    if (!aligned(o, 16) || !aligned(z, 16) || !aligned(w, 16) || !aligned(out, 16)) return GDN_ERR_INVALID_ARG;
+    const int64_t width = (int64_t)pool->view.h_v * pool->view.d;
+    if (n_tok > 1)
+        for (const int64_t ld : {ld_o, ld_z, ld_out})
+            if (ld < width || ld % 8 != 0) return GDN_ERR_INVALID_ARG;
+    return launch_gated_norm(pool, n_tok, o, ld_o, z, ld_z, w, eps, out_dtype, out, ld_out,
+                             as_stream(stream)) == hipSuccess
+               ? GDN_OK
+               : GDN_ERR_HIP;
+}
+
+static gdn_status mx_format_args(int64_t rows, int32_t cols, gdn_dtype dtype) {
+    if (rows < 0 || cols < 1 || !dtype_ok(dtype)) return GDN_ERR_INVALID_ARG;
+    if (cols % GDN_MX_GROUP != 0) return GDN_ERR_UNSUPPORTED;
+    return rows > INT64_MAX / cols / 4 ? GDN_ERR_INVALID_ARG : GDN_OK;
+}
+
+gdn_status gdn_mx_quantize(int64_t rows, int32_t cols, gdn_dtype dtype, const void* src, void* codes,
+                           uint8_t* scales, void* stream) {
+    const gdn_status st = mx_format_args(rows, cols, dtype);
+    if (st != GDN_OK) return st;
+    if (rows == 0) return GDN_OK;
+    if (!src || !codes || !scales || !aligned(src, 16) || !aligned(codes, 16)) return GDN_ERR_INVALID_ARG;
+    return launch_mx_quantize(rows, cols, dtype, src, codes, scales, as_stream(stream)) == hipSuccess
+               ? GDN_OK
+               : GDN_ERR_HIP;
+}
+
+gdn_status gdn_mx_dequantize(int64_t rows, int32_t cols, const void* codes, const uint8_t* scales,
+                             gdn_dtype dtype, void* dst, void* stream) {
+    const gdn_status st = mx_format_args(rows, cols, dtype);
+    if (st != GDN_OK) return st;
+    if (rows == 0) return GDN_OK;
+    if (!dst || !codes || !scales || !aligned(dst, 16) || !aligned(codes, 16)) return GDN_ERR_INVALID_ARG;
+    return launch_mx_dequantize(rows, cols, dtype, codes, scales, dst, as_stream(stream)) == hipSuccess
+               ? GDN_OK
+               : GDN_ERR_HIP;
+}
+
+static gdn_status mx_proj_args(int64_t n_tok, int32_t n_in, int64_t n_out) {
+    if (n_tok < 0 || n_in < 1 || n_out < 1) return GDN_ERR_INVALID_ARG;
+    if (n_in % GDN_MX_GROUP != 0 || n_in > GDN_MX_MAX_IN || n_out > INT32_MAX - 256 ||
+        !mx_proj_fits(n_tok, n_out))
+        return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+// Output channels of the in-projection of a pool's layer.
+static int64_t mx_in_proj_channels(const gdn_pool* pool, bool with_z) {
+    const PoolView& P = pool->view;
+    return (int64_t)P.c_conv + (with_z ? (int64_t)P.h_v * P.d : 0) + 2 * (int64_t)P.h_v;
+}
+
+static gdn_status mx_workspace_ok(size_t need, const void* workspace, size_t workspace_bytes) {
+    if (workspace_bytes < need || (need > 0 && !workspace)) return GDN_ERR_WORKSPACE;
+    return workspace && !aligned(workspace, kAlign) ? GDN_ERR_INVALID_ARG : GDN_OK;
+}
+
+gdn_status gdn_mx_proj_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out, size_t* bytes) {
+    const gdn_status st = mx_proj_args(n_tok, n_in, n_out);
+    if (st != GDN_OK) return st;
+    if (!bytes) return GDN_ERR_INVALID_ARG;
+    *bytes = mx_proj_workspace_bytes(n_tok, n_in, n_out);
+    return GDN_OK;
+}
+
+gdn_status gdn_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
+                       const void* codes, const uint8_t* scales, gdn_dtype y_dtype, void* y, int64_t ld_y,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    gdn_status st = mx_proj_args(n_tok, n_in, n_out);
+    if (st != GDN_OK) return st;
+    if (!dtype_ok(y_dtype)) return GDN_ERR_INVALID_ARG;
+    if (n_tok == 0) return GDN_OK;
+    if (!x || !codes || !scales || !y) return GDN_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(y, elem_bytes(y_dtype))) return GDN_ERR_INVALID_ARG;
+    if (n_tok == 1) {   // a single row has no stride
+        ld_x = n_in;
+        ld_y = n_out;
+    }
+    if (ld_x < n_in || ld_x % 8 != 0 || ld_y < n_out) return GDN_ERR_INVALID_ARG;
+    if (ld_x > 2 * GDN_MX_MAX_IN) return GDN_ERR_UNSUPPORTED;
+    st = mx_workspace_ok(mx_proj_workspace_bytes(n_tok, n_in, n_out), workspace, workspace_bytes);
+    if (st != GDN_OK) return st;
+    return launch_mx_proj(n_tok, n_in, n_out, x, ld_x, codes, scales, y_dtype, y, ld_y, workspace,
+                          as_stream(stream)) == hipSuccess
+               ? GDN_OK
+               : GDN_ERR_HIP;
+}
+
+gdn_status gdn_mx_in_proj_workspace_bytes(const gdn_pool* pool, int64_t n_tok, int32_t hidden,
+                                          int32_t with_z, size_t* bytes) {
+    if (!pool) return GDN_ERR_INVALID_ARG;
+    const int64_t n_out = mx_in_proj_channels(pool, with_z != 0);
+    const gdn_status st = mx_proj_args(n_tok, hidden, n_out);
+    if (st != GDN_OK) return st;
+    if (!bytes) return GDN_ERR_INVALID_ARG;
+    *bytes = mx_proj_workspace_bytes(n_tok, hidden, (int32_t)n_out);
+    return GDN_OK;
+}
+
+gdn_status gdn_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
+                          const void* codes, const uint8_t* scales, void* q, void* k, void* v, void* z,
+                          float* a, float* b, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!pool) return GDN_ERR_INVALID_ARG;
+    const int64_t n_out = mx_in_proj_channels(pool, z != nullptr);
+    gdn_status st = mx_proj_args(n_tok, hidden, n_out);
+    if (st != GDN_OK) return st;
+    if (n_tok == 0) return GDN_OK;
+    if (!x || !codes || !scales || !q || !k || !v || !a || !b) return GDN_ERR_INVALID_ARG;
+    const size_t io = (size_t)pool->io_size;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(q, io) || !aligned(k, io) || !aligned(v, io) ||
+        !aligned(z, io) || !aligned(a, 4) || !aligned(b, 4))
+        return GDN_ERR_INVALID_ARG;
+    st = mx_workspace_ok(mx_proj_workspace_bytes(n_tok, hidden, (int32_t)n_out), workspace, workspace_bytes);
+    if (st != GDN_OK) return st;
+    return launch_mx_in_proj(pool, n_tok, hidden, x, codes, scales, q, k, v, z, a, b, workspace,
+                             as_stream(stream)) == hipSuccess
+               ? GDN_OK
+               : GDN_ERR_HIP;
+}
+
 gdn_status gdn_pool_error(gdn_pool* pool, void* stream, int32_t* device_error) {
     if (!pool || !device_error) return GDN_ERR_INVALID_ARG;
     hipStream_t s = as_stream(stream);

@@ -182,6 +182,28 @@ size_t in_proj_workspace_bytes(const gdn_pool* pool, int64_t n_tok, int32_t hidd
 hipError_t launch_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
                           const void* w, void* q, void* k, void* v, float* a, float* b,
                           void* workspace, hipStream_t stream);
+// Norms around the core.
+hipError_t launch_block_norm(int64_t n_tok, int32_t hidden, gdn_dtype io_dtype, gdn_dtype res_dtype,
+                             const void* y, int64_t ld_y, const float* w_post, float res_scale,
+                             const void* r, int64_t ld_r, void* r_out, int64_t ld_ro,
+                             const float* w_pre, float w_offset, float eps, void* x, int64_t ld_x,
+                             hipStream_t stream);
+hipError_t launch_gated_norm(const gdn_pool* pool, int64_t n_tok, const void* o, int64_t ld_o,
+                             const void* z, int64_t ld_z, const float* w, float eps,
+                             gdn_dtype out_dtype, void* out, int64_t ld_out, hipStream_t stream);
+// 4-bit weights: the format and the projections.
+hipError_t launch_mx_quantize(int64_t rows, int32_t cols, gdn_dtype dtype, const void* src, void* codes,
+                              uint8_t* scales, hipStream_t stream);
+hipError_t launch_mx_dequantize(int64_t rows, int32_t cols, gdn_dtype dtype, const void* codes,
+                                const uint8_t* scales, void* dst, hipStream_t stream);
+bool mx_proj_fits(int64_t n_tok, int64_t n_out);
+size_t mx_proj_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out);
+hipError_t launch_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
+                          const void* codes, const uint8_t* scales, gdn_dtype y_dtype, void* y,
+                          int64_t ld_y, void* workspace, hipStream_t stream);
+hipError_t launch_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
+                             const void* codes, const uint8_t* scales, void* q, void* k, void* v,
+                             void* z, float* a, float* b, void* workspace, hipStream_t stream);
 size_t prefill_workspace_bytes(const gdn_pool* pool, int32_t n_seq, int64_t total_tokens,
                                int32_t chunk);
 // The static prefill scratch (kStaticScratchBytes on every device): its

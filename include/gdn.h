@@ -340,6 +340,101 @@ gdn_status gdn_in_proj(gdn_pool* pool, int64_t n_tok, int32_t hidden, const void
                        void* q, void* k, void* v, float* a, float* b, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* Block norm: closes one block and opens the next.  With the block's output y
+ * and the residual stream res,
+ *     u       = y,  or  w_post * y / sqrt(mean(y^2) + eps)  with w_post given
+ *     res_out = res + res_scale * u
+ *     x       = (w_offset + w_pre) * r / sqrt(mean(r^2) + eps),
+ * r being res + res_scale * u before it is rounded to the residual's type,
+ * means over the hidden size, all arithmetic in fp32.
+ *   y        device io_dtype [n_tok][hidden], or NULL: nothing is added (res is
+ *            normalised as it is; res_out and w_post must then be NULL)
+ *   w_post   device fp32 [hidden], or NULL
+ *   res      device res_dtype [n_tok][hidden]
+ *   res_out  device res_dtype [n_tok][hidden]
+ *   w_pre    device fp32 [hidden]; w_offset 1 serves weights stored as w - 1
+ *   x        device io_dtype [n_tok][hidden]
+ * Each ld is the stride in elements between an operand's rows (at least
+ * hidden; not read for a single row).  res_out may be res, and x may be y or
+ * res, with the same type and stride; operands must not overlap otherwise.
+ * Any hidden size up to GDN_BLOCK_NORM_MAX_HIDDEN (above: UNSUPPORTED) and any
+ * element alignment are taken; 16-byte aligned rows of a multiple of eight
+ * elements are read and written in 16-byte vectors. */
+#define GDN_BLOCK_NORM_MAX_HIDDEN 16384
+gdn_status gdn_block_norm(int64_t n_tok, int32_t hidden, gdn_dtype io_dtype, gdn_dtype res_dtype,
+                          const void* y, int64_t ld_y, const float* w_post, float res_scale,
+                          const void* res, int64_t ld_res, void* res_out, int64_t ld_res_out,
+                          const float* w_pre, float w_offset, float eps, void* x, int64_t ld_x,
+                          void* stream);
+
+/* Gated head norm, the step behind the core: per token and value head
+ *     out = w * o / sqrt(mean(o^2) + eps) * z * sigmoid(z)
+ * with the mean over the head's d_v elements and fp32 arithmetic.
+ *   o, z   device io dtype [n_tok][h_v][d_v]: the core's outputs and the gate
+ *   w      device fp32 [d_v]
+ *   out    device out_dtype [n_tok][h_v][d_v]
+ * ld_o, ld_z and ld_out are the strides in elements between tokens (at least
+ * h_v*d_v and multiples of 8; not read for a single token); all pointers are
+ * 16-byte aligned.  out may be o or z with the same type and stride.  The
+ * pool supplies the shapes only; no slot is read or written. */
+gdn_status gdn_gated_norm(const gdn_pool* pool, int64_t n_tok, const void* o, int64_t ld_o, const void* z,
+                          int64_t ld_z, const float* w, float eps, gdn_dtype out_dtype, void* out,
+                          int64_t ld_out, void* stream);
+
+/* 4-bit weights.  Groups of GDN_MX_GROUP consecutive weights of a row share one
+ * scale byte s, worth 2^(s - 127); 255 marks a group that held an infinity or a
+ * NaN (all its weights are NaN).  A weight is a 4-bit float: sign, two exponent
+ * bits, one fraction bit, i.e. 0, 0.5, 1, 1.5, 2, 3, 4 or 6 with a sign.
+ *   codes   device [rows][cols/2] bytes (16-byte aligned), the weight of the
+ *           even column in the low half of its byte
+ *   scales  device [rows][cols/32] bytes
+ * This is the microscaling format with 4-bit (e2m1) elements, as stored by
+ * checkpoints that use it.  cols must be a multiple of GDN_MX_GROUP
+ * (UNSUPPORTED otherwise).
+ *
+ * gdn_mx_quantize: src (device, dtype, [rows][cols] contiguous, 16-byte
+ * aligned) to codes and scales.  s - 127 is floor(log2(largest magnitude of
+ * the group)) - 2, at least -127 (a group of zeros: 0); codes are the weight
+ * over the scale rounded to nearest, ties to the even code, saturating at 6.
+ * gdn_mx_dequantize: back to dst (device, dtype, [rows][cols], 16-byte
+ * aligned), exactly (weights past the largest finite value become infinite),
+ * e.g. for gdn_in_proj, which takes bf16 weights. */
+#define GDN_MX_GROUP 32
+gdn_status gdn_mx_quantize(int64_t rows, int32_t cols, gdn_dtype dtype, const void* src, void* codes,
+                           uint8_t* scales, void* stream);
+gdn_status gdn_mx_dequantize(int64_t rows, int32_t cols, const void* codes, const uint8_t* scales,
+                             gdn_dtype dtype, void* dst, void* stream);
+
+/* Projection with 4-bit weights: y = x W^T, W as above with n_out rows of n_in
+ * weights; products are exact and accumulate in fp32.
+ *   x          device bf16 [n_tok][n_in], 16-byte aligned, ld_x elements
+ *              between rows (a multiple of 8, at least n_in)
+ *   y          device y_dtype [n_tok][n_out], ld_y elements between rows
+ *   workspace  device, >= gdn_mx_proj_workspace_bytes (0 for most sizes: NULL
+ *              will do then), 256-byte aligned; scratch only
+ * A single row's strides are not read.  Any n_out and n_tok; n_in a multiple
+ * of GDN_MX_GROUP up to GDN_MX_MAX_IN, ld_x up to twice that, and fewer than
+ * 2^23 tiles of 64 tokens by 64 channels (UNSUPPORTED otherwise). */
+#define GDN_MX_MAX_IN 1048576
+gdn_status gdn_mx_proj_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out, size_t* bytes);
+gdn_status gdn_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
+                       const void* codes, const uint8_t* scales, gdn_dtype y_dtype, void* y, int64_t ld_y,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* gdn_in_proj with 4-bit weights, and the gate z of gdn_gated_norm beside the
+ * core's inputs: the rows of W are q heads | k heads | v heads | z heads (only
+ * with z given) | h_v a logits | h_v b logits.
+ *   x          device bf16 [n_tok][hidden] (16-byte aligned)
+ *   q, k, v    as in gdn_in_proj; z device io dtype [n_tok][h_v][d_v], or NULL
+ *   a, b       device fp32 [n_tok][h_v]: a = exp(-softplus(y_a)),
+ *              b = sigmoid(y_b)
+ * Sizes and workspace as for gdn_mx_proj.  The pool supplies the shapes only. */
+gdn_status gdn_mx_in_proj_workspace_bytes(const gdn_pool* pool, int64_t n_tok, int32_t hidden,
+                                          int32_t with_z, size_t* bytes);
+gdn_status gdn_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
+                          const void* codes, const uint8_t* scales, void* q, void* k, void* v, void* z,
+                          float* a, float* b, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then read and clear the sticky device error word
  * (0 = none; bit 0 = a slot id >= n_slots was skipped; bit 1 = a malformed
  * cu_seqlens was seen). */
