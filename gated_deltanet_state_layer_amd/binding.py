@@ -125,9 +125,7 @@ def _check(status: int, what: str):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, name, numel, dtype):
@@ -139,7 +137,7 @@ def _need(t, name, numel, dtype):
         return
     if t is None:
         raise ValueError(f"{name}: missing")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: not a device tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
@@ -149,10 +147,17 @@ def _need(t, name, numel, dtype):
         raise ValueError(f"{name}: {t.numel()} elements, the call needs {numel}")
 
 
+# The current stream's handle without a Stream object around it: 0.2 us of a
+# call's host time in place of 2.9 us, the largest share of a small call's 11.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _io_torch(io_dtype: int):
@@ -206,11 +211,11 @@ def _rows(t, name, shape, dtype):
     elements between rows."""
     if t is None:
         raise ValueError(f"{name}: missing")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: not a device tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_contiguous():
         return t.numel() // shape[0] if shape[0] else 0
@@ -295,7 +300,7 @@ def mx_proj(x, codes, scales, out, workspace=None, stream=None):
     code = _dtype(out, "out")
     _need(codes, "codes", n_out * n_in // 2, torch.uint8)
     _need(scales, "scales", n_out * n_in // GDN_MX_GROUP, torch.uint8)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = 0 if workspace is None else workspace.nbytes
     _check(lib.gdn_mx_proj(n_tok, n_in, n_out, _ptr(x), ld_x, _ptr(codes), _ptr(scales), code,
                            _ptr(out), ld_y, _ptr(workspace), ws_bytes, _stream(stream)),
            "gdn_mx_proj")
@@ -448,7 +453,7 @@ class Pool:
         _need(v, "v", n_tok * d.h_v * d.d_v, self.io_torch)
         _need(a, "a", n_tok * d.h_v, torch.float32)
         _need(b, "b", n_tok * d.h_v, torch.float32)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_bytes = 0 if workspace is None else workspace.nbytes
         _check(lib.gdn_in_proj(self._h, n_tok, hidden, _ptr(x), _ptr(w), _ptr(q), _ptr(k), _ptr(v),
                                _ptr(a), _ptr(b), _ptr(workspace), ws_bytes, _stream(stream)),
                "gdn_in_proj")
@@ -465,7 +470,7 @@ class Pool:
         lib = load_library()
         n_seq = int(slot_ids.numel())
         self._prefill_args(n_seq, cu_seqlens, slot_ids, total_tokens, q, k, v, a, b, conv_w, out)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_bytes = 0 if workspace is None else workspace.nbytes
         _check(lib.gdn_prefill_chunked(self._h, layer, n_seq, _ptr(cu_seqlens), _ptr(slot_ids),
                                        total_tokens, chunk, _ptr(q), _ptr(k), _ptr(v), _ptr(a),
                                        _ptr(b), _ptr(conv_w), _ptr(out), _ptr(workspace), ws_bytes,
@@ -496,7 +501,7 @@ class Pool:
             _need(ckpt_offsets, "ckpt_offsets", n_seq + 1, torch.int32)
             _need(ckpt_slots, "ckpt_slots", 0 if ckpt_slots is None else ckpt_slots.numel(),
                   torch.int32)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_bytes = 0 if workspace is None else workspace.nbytes
         _check(lib.gdn_prefill_chunked_ckpt(self._h, layer, n_seq, _ptr(cu_seqlens),
                                             _ptr(slot_ids), total_tokens, chunk, _ptr(q), _ptr(k),
                                             _ptr(v), _ptr(a), _ptr(b), _ptr(conv_w), _ptr(out),
@@ -546,7 +551,7 @@ class Pool:
             _need(z, "z", n_tok * d.h_v * d.d_v, self.io_torch)
         _need(a, "a", n_tok * d.h_v, torch.float32)
         _need(b, "b", n_tok * d.h_v, torch.float32)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_bytes = 0 if workspace is None else workspace.nbytes
         _check(lib.gdn_mx_in_proj(self._h, n_tok, hidden, _ptr(x), _ptr(codes), _ptr(scales),
                                   _ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(a), _ptr(b),
                                   _ptr(workspace), ws_bytes, _stream(stream)), "gdn_mx_in_proj")

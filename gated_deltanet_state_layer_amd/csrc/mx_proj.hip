@@ -31,23 +31,35 @@ struct MxOut {
     int end[4];
     float *a, *b;
     int h_v, n_out;
-    int vec4, vec8;   // segment starts, strides and ends are multiples of 4 / 8 elements
+    int vec4, vec16;   // segment starts, strides and ends are multiples of 4 elements / 16 bytes
 };
 
+// The segments' values are picked lane by lane: an index would read them from
+// memory again.
 template <typename T>
 __device__ __forceinline__ T* mx_at(const MxOut& o, int64_t t, int n) {
-    int s = 0, base = 0;
+    void* p = o.seg[0];
+    int64_t ld = o.ld[0];
+    int base = 0;
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-        if (n >= o.end[i]) { s = i + 1; base = o.end[i]; }
-    return static_cast<T*>(o.seg[s]) + t * o.ld[s] + n - base;
+    for (int i = 0; i < 3; ++i) {
+        const bool past = n >= o.end[i];
+        p = past ? o.seg[i + 1] : p;
+        ld = past ? o.ld[i + 1] : ld;
+        base = past ? o.end[i] : base;
+    }
+    return static_cast<T*>(p) + t * ld + n - base;
 }
 
 template <typename T>
 __device__ __forceinline__ void mx_put(const MxOut& o, int64_t t, int n, float y) {
-    if (n < o.end[3]) Io<T>::store(mx_at<T>(o, t, n), 0, y);
-    else if (n < o.end[3] + o.h_v) o.a[t * o.h_v + n - o.end[3]] = 1.0f / (1.0f + expf(y));
-    else o.b[t * o.h_v + n - o.end[3] - o.h_v] = 1.0f / (1.0f + expf(-y));
+    if (n < o.end[3]) {
+        Io<T>::store(mx_at<T>(o, t, n), 0, y);
+        return;
+    }
+    const int g = n - o.end[3];
+    const bool is_b = g >= o.h_v;
+    (is_b ? o.b - o.h_v : o.a)[t * o.h_v + g] = 1.0f / (1.0f + expf(is_b ? -y : y));
 }
 
 __device__ __forceinline__ u32x2 pack4(f32x4 y) {
@@ -64,9 +76,12 @@ __device__ __forceinline__ void mx_put4(const MxOut& o, int64_t t, int n, f32x4 
         else *reinterpret_cast<f32x4*>(p) = y;
         return;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (n + i < o.n_out) mx_put<T>(o, t, n + i, y[i]);
+    const int end = min(4, o.n_out - n);
+#pragma unroll 1
+    for (int i = 0; i < end; ++i) {
+        mx_put<T>(o, t, n + i, y[0]);
+        y = f32x4{y[1], y[2], y[3], 0.f};
+    }
 }
 
 // Eight codes (one register) times their group's scale, in bf16.  A weight
@@ -78,6 +93,14 @@ __device__ __forceinline__ bf16x8 mx_expand(uint32_t c, float scale) {
     const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2);
     const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3);
     return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+}
+
+// An offset, or one past every descriptor.  Opaque to the compiler, which would
+// otherwise split the load into two branches with a wait between them.
+__device__ __forceinline__ int offset_if(bool in, int offset) {
+    int v = in ? offset : kOffOOB;
+    asm("" : "+v"(v));
+    return v;
 }
 
 struct MxIn {
@@ -110,32 +133,7 @@ __device__ __forceinline__ void transpose4(u32x4& w) {
     w = u32x4{c[0], c[1], d[0], d[1]};
 }
 
-// Largest over the four lanes 16 apart, in all four.
-__device__ __forceinline__ uint32_t max_over_rows(uint32_t x) {
-    const auto a = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    x = max((uint32_t)a[0], (uint32_t)a[1]);
-    const auto b = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    return max((uint32_t)b[0], (uint32_t)b[1]);
-}
-
-// The scale bytes of groups 4 st .. 4 st + 3 of a row, the first lowest.  The
-// load may be unaligned; where the row ends inside the four it starts earlier,
-// by scales_past() bytes that the caller shifts out once it has arrived.
-__device__ __forceinline__ int scales_past(int st, int groups) {
-    return groups < 4 ? 0 : max(0, st * 4 + 4 - groups);
-}
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* row, int st, int groups) {
-    uint32_t v = 0;
-    if (groups >= 4) {
-        __builtin_memcpy(&v, row + st * 4 - scales_past(st, groups), 4);
-    } else {
-#pragma unroll 1
-        for (int j = 0; j < groups; ++j) v |= (uint32_t)row[j] << (8 * j);
-    }
-    return v;
-}
-
-// Few tokens, and the strip of channels that the tile kernel leaves.  One
+// Few tokens, and the strip of gates that the tile kernel leaves.  One
 // workgroup of 8 waves per 16 NT tokens and 16 NC channels; each wave
 // multiplies the whole tile over its eighth of the input axis, operands
 // straight from memory, D steps of 128 in flight, and the eight partial tiles
@@ -143,8 +141,9 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* row, int st, int 
 // bytes (32 codes); transposed over q, MFMA j of the four (16x16x32) takes
 // group j, lane q its codes 8q .. 8q+7, so tokens are read 64 bytes at a time.
 // W is the A operand: a lane's four results are consecutive channels of one
-// token.  With SPLIT the workgroups of channel block 0 also write the tokens'
-// 8-bit split (NC = 0: nothing else).
+// token.  A row's last step may reach past it: its tokens read zeros there and
+// its scales are 0, so whatever the codes are adds nothing.  At least four
+// groups of 32 (the scale bytes of a step come as one word).
 constexpr int kSkinnyWaves = 8;
 constexpr int kSkinnyThreads = 64 * kSkinnyWaves;
 
@@ -152,58 +151,65 @@ constexpr size_t skinny_lds(int nt, int nc) {
     return (size_t)kSkinnyWaves * 16 * nt * (16 * nc + 4) * sizeof(float);
 }
 
-template <typename T, int NT, int NC, bool SPLIT>
-__global__ __launch_bounds__(kSkinnyThreads, NT * 16 + NC * 5 > 40 ? 2 : 4) void mx_skinny_kernel(MxIn p, MxOut o, int c0,
-                                                                                       MxSplit sp) {
+template <typename T, int NT, int NC>
+__device__ __forceinline__ void skinny_tile(const MxIn& p, const MxOut& o, int64_t t0, int n0) {
     constexpr int D = 2;
     extern __shared__ __align__(16) float red[];   // [8 waves][16 NT tokens][16 NC + 4 channels]
-    __shared__ uint32_t flags[16 * NT];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
-    const int64_t t0 = (int64_t)blockIdx.y * (16 * NT);
-    const int n0 = c0 + blockIdx.x * (16 * NC);
+    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int toks = (int)min((int64_t)(16 * NT), p.n_tok - t0), rows = min(16 * NC, p.n_out - n0);
     const int half = p.n_in / 2, groups = p.n_in / 32;
     const int steps = (groups + 3) / 4, per = (steps + kSkinnyWaves - 1) / kSkinnyWaves;
     const int s_begin = wave * per, s_end = min(steps, s_begin + per);
-    const bool split = SPLIT && blockIdx.x == 0;
     const auto x_rs = buf_rsrc(p.x + t0 * p.ld_x, ((toks - 1) * p.ld_x + p.n_in) * 2);
     const auto w_rs = buf_rsrc(p.codes + (int64_t)n0 * half, (int64_t)rows * half);
-    if constexpr (SPLIT) {
-        if (threadIdx.x < 16 * NT) flags[threadIdx.x] = 0;
-        __syncthreads();
+    const uint8_t* sc = p.scales + (int64_t)n0 * groups;
+    int wo[NC], xo[NT];
+    uint32_t so[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int r = c * 16 + m;
+        wo[c] = offset_if(r < rows, r * half + q * 16);
+        so[c] = (uint32_t)min(r, rows - 1) * (uint32_t)groups;
     }
-    u32x4 xs[D][NT][4], ws[D][NC > 0 ? NC : 1];
-    uint32_t ss[D][NC > 0 ? NC : 1];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = t * 16 + m;
+        xo[t] = offset_if(r < toks, (int)(r * p.ld_x + q * 8) * 2);
+    }
+    // The scale bytes of groups 4 st .. 4 st + 3, the first lowest.  The load may
+    // be unaligned; where the row ends inside the four it starts earlier, by
+    // past() bytes that are shifted out once it has arrived.
+    const auto past = [&](int st) { return max(0, st * 4 + 4 - groups); };
+    u32x4 xs[D][NT][4], ws[D][NC];
+    uint32_t ss[D][NC];
+    // steps from s_end on are loaded (the last one again) but not multiplied
     const auto fetch = [&](int st, int b) {
+        st = min(st, steps - 1);
+        const uint8_t* s = sc + (st * 4 - past(st));
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int r = c * 16 + m;
-            const bool in = st < s_end && r < rows;
-            ws[b][c] = __builtin_amdgcn_raw_buffer_load_b128(
-                w_rs, in && st * 4 + q < groups ? r * half + (st * 4 + q) * 16 : kOffOOB, 0, 0);
-            ss[b][c] = load_scales(p.scales + (int64_t)(n0 + min(r, rows - 1)) * groups, min(st, steps - 1), groups);
+            ws[b][c] = __builtin_amdgcn_raw_buffer_load_b128(w_rs, wo[c], st * 64, 0);
+            __builtin_memcpy(&ss[b][c], s + so[c], 4);
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = t * 16 + m;
-                const bool in = st < s_end && st * 4 + j < groups && r < toks;
+            for (int t = 0; t < NT; ++t)
                 xs[b][t][j] = __builtin_amdgcn_raw_buffer_load_b128(
-                    x_rs, in ? (int)(r * p.ld_x + st * 128 + j * 32 + q * 8) * 2 : kOffOOB, 0, 0);
-            }
+                    x_rs, offset_if(st * 4 + j < groups, xo[t]), min(st * 4 + j, groups - 1) * 64, 0);
     };
-    f32x4 acc[NT][NC > 0 ? NC : 1];
+    f32x4 acc[NT][NC];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     const auto multiply = [&](int st, int b) {
-        const int past = 8 * scales_past(st, groups);
+        const int shift = 8 * past(st);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             transpose4(ws[b][c]);
-            const uint32_t s = ss[b][c] >> past;
+            const uint32_t s = ss[b][c] >> shift;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bf16x8 wf = mx_expand(ws[b][c][j], __uint_as_float((s >> (8 * j) & 0xffu) << 23));
@@ -214,62 +220,14 @@ __global__ __launch_bounds__(kSkinnyThreads, NT * 16 + NC * 5 > 40 ? 2 : 4) void
             }
         }
     };
-    // The split of step st: lane (m, q) holds values 8q .. 8q+7 of group 4 st + j of token m.
-    const auto write_split = [&](int st, int b) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int r = t * 16 + m;
-            uint32_t packed = 0, flag = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top = max(top, max(xs[b][t][j][i] << 16 & 0x7fff0000u, xs[b][t][j][i] & 0x7fff0000u));
-                top = max_over_rows(top);
-                // the largest magnitude to [128, 256), scale bytes from 5 on (lo's is 5 less)
-                int e;
-                (void)frexpf(__uint_as_float(top), &e);   // top in [2^(e-1), 2^e)
-                const int s = top == 0 ? 127 : max(e - 8 + 127, 5);
-                const int up = 127 - s;
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float v0 = ldexpf(__uint_as_float(xs[b][t][j][i] << 16), up);
-                    const float v1 = ldexpf(__uint_as_float(xs[b][t][j][i] & 0xffff0000u), up);
-                    const int h = __builtin_amdgcn_cvt_pk_fp8_f32(v0, v1, 0, false);
-                    const f32x2 f = __builtin_amdgcn_cvt_pk_f32_fp8(h, false);
-                    const int l = __builtin_amdgcn_cvt_pk_fp8_f32((v0 - f[0]) * 32.0f, (v1 - f[1]) * 32.0f, 0, false);
-                    if (i & 1) { hi[i / 2] |= (uint32_t)h << 16; lo[i / 2] |= (uint32_t)l << 16; }
-                    else { hi[i / 2] = (uint32_t)h & 0xffffu; lo[i / 2] = (uint32_t)l & 0xffffu; }
-                }
-                const bool finite = top < 0x7f800000u;
-                packed |= (finite ? (uint32_t)s : 255u) << (8 * j);
-                flag |= finite ? 0u : top > 0x7f800000u ? 2u : 1u;
-                const int g = st * 4 + j;
-                if (r < toks && g * 64 < sp.row) {
-                    uint8_t* d = sp.data + (t0 + r) * sp.row + (g >> 1) * 128 + (g & 1) * 32 + q * 8;
-                    *reinterpret_cast<u32x2*>(d) = finite ? u32x2{hi[0], hi[1]} : u32x2{0, 0};
-                    *reinterpret_cast<u32x2*>(d + 64) = finite ? u32x2{lo[0], lo[1]} : u32x2{0, 0};
-                }
-            }
-            if (r < toks && q == 0) {
-                // rows hold an even number of groups
-                uint16_t* d = reinterpret_cast<uint16_t*>(sp.scales + (t0 + r) * (sp.row / 64)) + st * 2;
-                d[0] = (uint16_t)packed;
-                if (st * 4 + 2 < sp.row / 64) d[1] = (uint16_t)(packed >> 16);
-                if (flag) atomicOr(&flags[r], flag);
-            }
-        }
-    };
 #pragma unroll
     for (int i = 0; i < D; ++i) fetch(s_begin + i, i);
     __builtin_amdgcn_sched_barrier(0);
     int st = s_begin;
+#pragma unroll 1
     for (; st + D < s_end; st += D) {
 #pragma unroll
         for (int i = 0; i < D; ++i) {
-            if (split) write_split(st + i, i);
             multiply(st + i, i);
             fetch(st + D + i, i);
             __builtin_amdgcn_sched_barrier(0);
@@ -277,34 +235,98 @@ __global__ __launch_bounds__(kSkinnyThreads, NT * 16 + NC * 5 > 40 ? 2 : 4) void
     }
 #pragma unroll
     for (int i = 0; i < D; ++i)
-        if (st + i < s_end) {
-            if (split) write_split(st + i, i);
-            multiply(st + i, i);
-        }
-    if constexpr (NC > 0) {
-        constexpr int LD = 16 * NC + 4;
-        float* mine = red + wave * (16 * NT * LD);
+        if (st + i < s_end) multiply(st + i, i);
+    constexpr int LD = 16 * NC + 4;
+    float* mine = red + wave * (16 * NT * LD);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                *reinterpret_cast<f32x4*>(&mine[(t * 16 + m) * LD + c * 16 + 4 * q]) = acc[t][c];
-    }
+        for (int c = 0; c < NC; ++c)
+            *reinterpret_cast<f32x4*>(&mine[(t * 16 + m) * LD + c * 16 + 4 * q]) = acc[t][c];
     __syncthreads();
-    if constexpr (SPLIT) {
-        if (split && threadIdx.x < toks) sp.flags[t0 + threadIdx.x] = (uint8_t)flags[threadIdx.x];
-    }
-    if constexpr (NC > 0) {
-        constexpr int LD = 16 * NC + 4;
-        for (int i = threadIdx.x; i < 16 * NT * 4 * NC; i += kSkinnyThreads) {
-            const int t = i / (4 * NC), c = (i % (4 * NC)) * 4;
-            if (t >= toks || n0 + c >= p.n_out) continue;
-            f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int i = threadIdx.x; i < 16 * NT * 4 * NC; i += kSkinnyThreads) {
+        const int t = i / (4 * NC), c = (i % (4 * NC)) * 4;
+        if (t >= toks || n0 + c >= p.n_out) continue;
+        f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < kSkinnyWaves; ++w)
-                y += *reinterpret_cast<const f32x4*>(&red[w * (16 * NT * LD) + t * LD + c]);
-            mx_put4<T>(o, t0 + t, n0 + c, y);
+        for (int w = 0; w < kSkinnyWaves; ++w)
+            y += *reinterpret_cast<const f32x4*>(&red[w * (16 * NT * LD) + t * LD + c]);
+        mx_put4<T>(o, t0 + t, n0 + c, y);
+    }
+}
+
+constexpr int skinny_waves_per_simd(int nt, int nc) { return nt * 16 + nc * 5 > 40 ? 2 : 4; }
+
+template <typename T, int NT, int NC>
+__global__ __launch_bounds__(kSkinnyThreads, skinny_waves_per_simd(NT, NC)) void mx_skinny_kernel(MxIn p, MxOut o,
+                                                                                                  int cols) {
+    skinny_tile<T, NT, NC>(p, o, (int64_t)(blockIdx.x / cols) * (16 * NT), (int)(blockIdx.x % cols) * (16 * NC));
+}
+
+// The split of the tokens, one wave per token, 16 values per lane and round;
+// and in the first gate_wgs workgroups of the same launch the gates, which keep
+// fp32's accuracy: the skinny product over the strip of channels from c0 on.
+constexpr int kGateTokens = 1, kGateChannels = 4;   // in 16s
+
+__global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxOut o, int c0, int cols,
+                                                                     unsigned gate_wgs, MxSplit sp) {
+    if (blockIdx.x < gate_wgs) {
+        skinny_tile<uint16_t, kGateTokens, kGateChannels>(p, o, (int64_t)(blockIdx.x / cols) * (16 * kGateTokens),
+                                                          c0 + (int)(blockIdx.x % cols) * (16 * kGateChannels));
+        return;
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, values = sp.row / 2;
+    const int64_t stride = (int64_t)(gridDim.x - gate_wgs) * kSkinnyWaves;
+    for (int64_t t = (int64_t)(blockIdx.x - gate_wgs) * kSkinnyWaves + wave; t < p.n_tok; t += stride) {
+        const uint16_t* x = p.x + t * p.ld_x;
+        uint32_t flag = 0;
+        u32x4 next[2];
+        const auto load = [&](int v) {
+            next[0] = next[1] = u32x4{0, 0, 0, 0};
+            if (v < p.n_in) {
+                next[0] = *reinterpret_cast<const u32x4*>(x + v);
+                next[1] = *reinterpret_cast<const u32x4*>(x + v + 8);
+            }
+        };
+        load(lane * 16);
+        for (int v0 = 0; v0 < values; v0 += 64 * 16) {
+            const int v = v0 + lane * 16;
+            const u32x4 in[2] = {next[0], next[1]};
+            load(v + 64 * 16);
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                top = max(top, max(in[i / 4][i % 4] << 16 & 0x7fff0000u, in[i / 4][i % 4] & 0x7fff0000u));
+            // two lanes hold a group
+            top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, false));
+            // the largest magnitude to [128, 256), scale bytes from 5 on (lo's is 5 less)
+            int e;
+            (void)frexpf(__uint_as_float(top), &e);   // top in [2^(e-1), 2^e)
+            const int s = top == 0 ? 127 : max(e - 8 + 127, 5);
+            const bool finite = top < 0x7f800000u;
+            u32x4 hi, lo;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = ldexpf(__uint_as_float(in[i / 4][i % 4] << 16), 127 - s);
+                const float b = ldexpf(__uint_as_float(in[i / 4][i % 4] & 0xffff0000u), 127 - s);
+                const int h = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+                const f32x2 f = __builtin_amdgcn_cvt_pk_f32_fp8(h, false);
+                const int l = __builtin_amdgcn_cvt_pk_fp8_f32((a - f[0]) * 32.0f, (b - f[1]) * 32.0f, 0, false);
+                if (i & 1) { hi[i / 2] |= (uint32_t)h << 16; lo[i / 2] |= (uint32_t)l << 16; }
+                else { hi[i / 2] = (uint32_t)h & 0xffffu; lo[i / 2] = (uint32_t)l & 0xffffu; }
+            }
+            if (v < values) {
+                uint8_t* d = sp.data + t * sp.row + (v >> 6) * 128 + (v & 63);
+                const u32x4 zero = {0, 0, 0, 0};
+                *reinterpret_cast<u32x4*>(d) = finite ? hi : zero;
+                *reinterpret_cast<u32x4*>(d + 64) = finite ? lo : zero;
+                if ((lane & 1) == 0) sp.scales[t * (sp.row / 64) + (v >> 5)] = (uint8_t)(finite ? s : 255);
+            }
+            flag |= finite ? 0u : top > 0x7f800000u ? 2u : 1u;
         }
+        const bool inf = __ballot(flag & 1) != 0, nan = __ballot(flag & 2) != 0;
+        if (lane == 0) sp.flags[t] = (uint8_t)((inf ? 1 : 0) | (nan ? 2 : 0));
     }
 }
 
@@ -335,8 +357,8 @@ struct TileShape {
     static constexpr int kScale = 3 * kStage;            // two stages of CC * 2 + TT * 2 bytes
     static constexpr int kBytes = kScale + 2 * 2 * (CC + TT);
     static_assert(TT * 2 == TH && CC * 2 == TH, "per thread one scale byte of each operand, and 4 + 1 loads");
-    // the epilogue's rows (bf16, 16 bytes apart) in the stages
-    static constexpr int kRow = 16 * NC * 2 + 16;
+    // the epilogue's rows (fp32, 16 bytes apart) in the stages
+    static constexpr int kRow = 16 * NC * 4 + 16;
     static_assert(WT * WC * 16 * kRow <= 3 * kStage, "epilogue rows fit");
 };
 
@@ -384,7 +406,8 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
                                                                   int n_end) {
     using S = TileShape<F8, NT, NC, WT, WC>;
     extern __shared__ __align__(16) uint8_t lds[];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, q = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wt = wave / WC, wc = wave % WC;
     // consecutive tiles share their channels
     const int64_t t0 = (int64_t)(blockIdx.x % tiles_t) * S::TT;
@@ -406,31 +429,34 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
     for (int i = 0; i < 4; ++i) {
         const int r = wave * 32 + i * 8 + (lane >> 3);
         xchunk[i] = (lane & 7) ^ ((r >> 1) & 7);
-        gx[i] = r < toks ? (F8 ? r * sp.row : (int)(r * p.ld_x * 2)) + xchunk[i] * 16 : kOffOOB;
+        gx[i] = offset_if(r < toks, (F8 ? r * sp.row : (int)(r * p.ld_x * 2)) + xchunk[i] * 16);
     }
     const int wrow = wave * 32 + (lane >> 1), wchunk = (lane & 1) ^ ((wrow >> 3) & 1);
-    const int gw = wrow < rows ? wrow * half + wchunk * 16 : kOffOOB;
-    const auto issue = [&](int kb, int st) {
+    const int gw = offset_if(wrow < rows, wrow * half + wchunk * 16);
+    // Past a row's end the tokens are zeros (or the split's padding) and the
+    // scales 0, so the codes there may be anything; past the last block it is
+    // loaded again and not used.  Scalar offsets stay inside the descriptors:
+    // their range is checked on what is left behind that offset.
+    const auto issue = [&](int k, int st) {
+        const int kb = min(k, blocks - 1);
         uint8_t* base = lds + st * S::kStage;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool in = gx[i] != kOffOOB && (F8 ? kb < blocks : kb * 64 + xchunk[i] * 8 < p.n_in);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(x_rs, (lds_ptr)(base + (wave * 4 + i) * 1024), 16,
-                                                     in ? gx[i] + kb * 128 : kOffOOB, 0, 0, 0);
-        }
-        const bool in = gw != kOffOOB && kb * 2 + wchunk < groups;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rs, (lds_ptr)(base + S::kX + wave * 1024), 16,
-                                                 in ? gw + kb * 32 : kOffOOB, 0, 0, 0);
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                x_rs, (lds_ptr)(base + (wave * 4 + i) * 1024), 16,
+                F8 ? gx[i] : offset_if(kb * 64 + xchunk[i] * 8 < p.n_in, gx[i]), kb * 128, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rs, (lds_ptr)(base + S::kX + wave * 1024), 16, gw, kb * 32, 0, 0);
     };
     // Scale bytes: thread tid carries group tid % 2 of row tid / 2.
     const int srow = tid >> 1, sgrp = tid & 1;
     uint32_t sw_in, sx_in = 0;
     const auto issue_scales = [&](int kb) {
         const int g = kb * 2 + sgrp;
-        sw_in = __builtin_amdgcn_raw_buffer_load_b8(s_rs, srow < rows && g < groups ? srow * groups + g : kOffOOB, 0, 0);
+        sw_in = __builtin_amdgcn_raw_buffer_load_b8(
+            s_rs, offset_if((srow < rows) & (g < groups), srow * groups + g), 0, 0);
         if constexpr (F8)
             sx_in = __builtin_amdgcn_raw_buffer_load_b8(
-                e_rs, srow < toks && kb < blocks ? srow * (sp.row / 64) + g : kOffOOB, 0, 0);
+                e_rs, offset_if((srow < toks) & (kb < blocks), srow * (sp.row / 64) + g), 0, 0);
     };
     const int sw_at = ((srow / (16 * NC) * 16 + (srow & 15)) * 2 + sgrp) * NC + (srow >> 4) % NC;
     const int sx_at = 2 * S::CC + ((srow / (16 * NT) * 16 + (srow & 15)) * 2 + sgrp) * NT + (srow >> 4) % NT;
@@ -544,63 +570,56 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
     __builtin_amdgcn_s_waitcnt(0x0070);                          // vmcnt(0) lgkmcnt(0)
     __syncthreads();
 
+    // 16 tokens at a time through LDS, each wave its own rows, so that a token's
+    // channels leave in 16-byte pieces side by side
+    constexpr int V = 16 / (int)sizeof(T), PIECES = 16 * NC / V;
     const int64_t tw = t0 + wt * 16 * NT;
     const int nw = n0 + wc * 16 * NC;
-    if constexpr (sizeof(T) == 2) {
-        // 16 tokens at a time through LDS, each wave its own rows, so that a
-        // token's channels leave in 16-byte pieces side by side
-        uint8_t* eb = lds + wave * (16 * S::kRow);
+    const int end = min(n_end, o.end[3]);   // from here on gates
+    uint8_t* eb = lds + wave * (16 * S::kRow);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int n = nw + c * 16 + 4 * q;
-                if (F8 || n < o.end[3])
-                    *reinterpret_cast<u32x2*>(eb + m * S::kRow + (c * 16 + 4 * q) * 2) = pack4(acc[t][c]);
-                else if (n < n_end && tw + t * 16 + m < p.n_tok)
-                    mx_put4<T>(o, tw + t * 16 + m, n, acc[t][c]);   // gates: fp32
-            }
-#pragma unroll
-            for (int i = lane; i < 32 * NC; i += 64) {
-                const int r = i / (2 * NC), c8 = (i % (2 * NC)) * 8;
-                const u32x4 v = *reinterpret_cast<const u32x4*>(eb + r * S::kRow + c8 * 2);
-                const int64_t tok = tw + t * 16 + r;
-                const int n = nw + c8;
-                const int end = F8 ? n_end : min(n_end, o.end[3]);
-                if (tok >= p.n_tok || n >= end) continue;
-                uint32_t nan = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    nan |= (uint32_t)((v[j / 2] >> (16 * (j & 1)) & 0x7fffu) > 0x7f80u) << j;
-                if (o.vec8 && n + 8 <= end) {
-                    *reinterpret_cast<u32x4*>(mx_at<T>(o, tok, n)) = v;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (n + j < end) mx_put<T>(o, tok, n + j, __uint_as_float(v[j / 2] >> (16 * (j & 1)) << 16));
-                }
-                // A token with an infinity (and no NaN) has no split: its
-                // results are infinite or NaN, as the definition has them.
-                if constexpr (F8) {
-                    if (nan && sp.flags[tok] == 1) {
+        for (int c = 0; c < NC; ++c)
+            *reinterpret_cast<f32x4*>(eb + m * S::kRow + (c * 16 + 4 * q) * 4) = acc[t][c];
 #pragma unroll 1
-                        for (; nan; nan &= nan - 1) {
-                            const int j = __ffs((int)nan) - 1;
-                            if (n + j < n_end) mx_put<T>(o, tok, n + j, mx_dot(p, tok, n + j));
-                        }
-                    }
+        for (int i = lane; i < 16 * PIECES; i += 64) {
+            const int r = i / PIECES, piece = (i % PIECES) * V;
+            const float* src = reinterpret_cast<const float*>(eb + r * S::kRow) + piece;
+            const int64_t tok = tw + t * 16 + r;
+            const int n = nw + piece;
+            if (tok >= p.n_tok || n >= n_end) continue;
+            const f32x4 y0 = *reinterpret_cast<const f32x4*>(src);
+            const f32x4 y1 = *reinterpret_cast<const f32x4*>(src + V - 4);
+            bool whole = o.vec16 && n + V <= end;
+            // A token with an infinity (and no NaN) has no split: its results
+            // are infinite or NaN, as the definition has them.
+            bool again = false;
+            if constexpr (F8) {
+                bool nan = false;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) nan |= (y0[j] != y0[j]) | (y1[j] != y1[j]);
+                again = nan && sp.flags[tok] == 1;
+            }
+            if (whole && !again) {
+                T* d = mx_at<T>(o, tok, n);
+                if constexpr (V == 8) {
+                    const u32x2 a = pack4(y0), b = pack4(y1);
+                    *reinterpret_cast<u32x4*>(d) = u32x4{a[0], a[1], b[0], b[1]};
+                } else {
+                    *reinterpret_cast<f32x4*>(d) = y0;
                 }
+                continue;
+            }
+            const int last = min(V, n_end - n);
+#pragma unroll 1
+            for (int j = 0; j < last; ++j) {
+                float y = src[j];
+                if constexpr (F8)
+                    if (again && y != y) y = mx_dot(p, tok, n + j);
+                mx_put<T>(o, tok, n + j, y);
             }
         }
-    } else {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int64_t tok = tw + t * 16 + m;
-                const int n = nw + c * 16 + 4 * q;
-                if (tok < p.n_tok && n < n_end) mx_put4<T>(o, tok, n, acc[t][c]);
-            }
     }
 }
 
@@ -608,17 +627,29 @@ bool fits(const void* p, int64_t ld, int elem, int vec) {
     return reinterpret_cast<uintptr_t>(p) % (vec * elem) == 0 && ld % vec == 0;
 }
 
-template <typename T, int NT, int NC, bool SPLIT>
-hipError_t skinny(const MxIn& p, const MxOut& o, int c0, const MxSplit& sp, hipStream_t stream) {
-    constexpr size_t lds = NC > 0 ? skinny_lds(NT, NC) : 0;
+template <typename T, int NT, int NC>
+hipError_t skinny(const MxIn& p, const MxOut& o, hipStream_t stream) {
+    constexpr size_t lds = skinny_lds(NT, NC);
     if (lds > 65536) {
         static std::atomic<uint64_t> done{0};
-        const hipError_t e = allow_dynamic_lds(&mx_skinny_kernel<T, NT, NC, SPLIT>, lds, &done);
+        const hipError_t e = allow_dynamic_lds(&mx_skinny_kernel<T, NT, NC>, lds, &done);
         if (e != hipSuccess) return e;
     }
-    const int cols = NC > 0 ? (p.n_out - c0 + 16 * NC - 1) / (16 * NC) : 1;
-    const dim3 grid((unsigned)cols, (unsigned)((p.n_tok + 16 * NT - 1) / (16 * NT)));
-    hipLaunchKernelGGL((mx_skinny_kernel<T, NT, NC, SPLIT>), grid, dim3(kSkinnyThreads), lds, stream, p, o, c0, sp);
+    const int cols = (p.n_out + 16 * NC - 1) / (16 * NC);
+    const dim3 grid((unsigned)(cols * ((p.n_tok + 16 * NT - 1) / (16 * NT))));
+    hipLaunchKernelGGL((mx_skinny_kernel<T, NT, NC>), grid, dim3(kSkinnyThreads), lds, stream, p, o, cols);
+    return hipGetLastError();
+}
+
+// The tokens' split and the channels from c0 on.
+hipError_t split(const MxIn& p, const MxOut& o, int c0, const MxSplit& sp, hipStream_t stream) {
+    constexpr size_t lds = skinny_lds(kGateTokens, kGateChannels);
+    static_assert(lds <= 65536, "the default limit");
+    const int cols = (p.n_out - c0 + 16 * kGateChannels - 1) / (16 * kGateChannels);
+    const int64_t gates = cols * ((p.n_tok + 16 * kGateTokens - 1) / (16 * kGateTokens));
+    const int64_t tokens = std::min<int64_t>((p.n_tok + kSkinnyWaves - 1) / kSkinnyWaves, 1 << 20);
+    hipLaunchKernelGGL(mx_split_kernel, dim3((unsigned)(gates + tokens)), dim3(kSkinnyThreads), gates ? lds : 0,
+                       stream, p, o, c0, cols, (unsigned)gates, sp);
     return hipGetLastError();
 }
 
@@ -655,7 +686,6 @@ MxSplit split_of(int64_t n_tok, int32_t n_in, void* workspace, size_t* bytes) {
 
 template <typename T>
 hipError_t launch_few(const MxIn& p, const MxOut& o, hipStream_t stream) {
-    const MxSplit none{};
     // Bytes that the busiest CU takes in, the tile's tokens and weights: the
     // measure that separates the shapes where the axis is not the limit.
     const auto cost = [&](int nt, int nc) {
@@ -671,27 +701,25 @@ hipError_t launch_few(const MxIn& p, const MxOut& o, hipStream_t stream) {
         if (c < least) { least = c; best = i; }
     }
     switch (best) {
-        case 0: return skinny<T, 1, 1, false>(p, o, 0, none, stream);
-        case 1: return skinny<T, 1, 2, false>(p, o, 0, none, stream);
-        case 2: return skinny<T, 1, 4, false>(p, o, 0, none, stream);
-        case 3: return skinny<T, 2, 2, false>(p, o, 0, none, stream);
-        case 4: return skinny<T, 2, 4, false>(p, o, 0, none, stream);
-        default: return skinny<T, 4, 4, false>(p, o, 0, none, stream);
+        case 0: return skinny<T, 1, 1>(p, o, stream);
+        case 1: return skinny<T, 1, 2>(p, o, stream);
+        case 2: return skinny<T, 1, 4>(p, o, stream);
+        case 3: return skinny<T, 2, 2>(p, o, stream);
+        case 4: return skinny<T, 2, 4>(p, o, stream);
+        default: return skinny<T, 4, 4>(p, o, stream);
     }
 }
 
 template <typename T>
 hipError_t launch_typed(const MxIn& p, const MxOut& o, void* workspace, hipStream_t stream) {
-    if (p.n_tok <= kSkinnyTokens) return launch_few<T>(p, o, stream);
+    if (p.n_tok <= kSkinnyTokens && p.n_in >= 128) return launch_few<T>(p, o, stream);
     const bool large = ((p.n_tok + 255) / 256) * ((p.n_out + 255) / 256) >= 256;
     if constexpr (sizeof(T) == 2) {
         if (use_split(p.n_tok, p.n_in, GDN_BF16)) {
             size_t bytes;
             const MxSplit sp = split_of(p.n_tok, p.n_in, workspace, &bytes);
-            // the gates keep fp32's accuracy: they go with the split's pass over the tokens
             const int n_end = o.end[3];
-            const hipError_t e = n_end < p.n_out ? skinny<T, 2, 4, true>(p, o, n_end, sp, stream)
-                                                 : skinny<T, 2, 0, true>(p, o, n_end, sp, stream);
+            const hipError_t e = split(p, o, n_end, sp, stream);
             if (e != hipSuccess) return e;
             return large ? tile<T, true, 4, 8, 4, 2>(p, o, sp, n_end, stream)
                          : tile<T, true, 4, 4, 2, 2>(p, o, sp, n_end, stream);
@@ -704,9 +732,11 @@ hipError_t launch_typed(const MxIn& p, const MxOut& o, void* workspace, hipStrea
 
 }  // namespace
 
-// Tiles of one launch (of 256 threads) stay below 2^32 threads.
+// Every launch stays below 2^32 threads: the most are 512 for each 16 tokens or
+// so and the few channels of the gates, or each 32 by 64.
 bool mx_proj_fits(int64_t n_tok, int64_t n_out) {
-    return ((n_tok + 63) / 64) * ((n_out + 63) / 64) < (1 << 23);
+    const int64_t t = n_tok / 64 + 1, c = n_out / 64 + 1;
+    return t < (1 << 22) && t * c < (1 << 22);
 }
 
 size_t mx_proj_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out) {
@@ -728,7 +758,7 @@ hipError_t launch_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void
     o.n_out = n_out;
     const int elem = y_dtype == GDN_BF16 ? 2 : 4;
     o.vec4 = n_out % 4 == 0 && fits(y, ld_y, elem, 4);
-    o.vec8 = n_out % 8 == 0 && fits(y, ld_y, elem, 8);
+    o.vec16 = n_out % (16 / elem) == 0 && fits(y, ld_y, elem, 16 / elem);
     return y_dtype == GDN_BF16 ? launch_typed<uint16_t>(p, o, workspace, stream)
                                : launch_typed<float>(p, o, workspace, stream);
 }
@@ -743,13 +773,13 @@ hipError_t launch_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden
     const int width[4] = {hkd, hkd, hvd, z ? hvd : 0};
     const int elem = pool->io_size;
     int end = 0;
-    o.vec4 = o.vec8 = 1;
+    o.vec4 = o.vec16 = 1;
     for (int i = 0; i < 4; ++i) {
         o.seg[i] = seg[i];
         o.ld[i] = width[i];
         o.end[i] = end += width[i];
         o.vec4 = o.vec4 && fits(seg[i], width[i], elem, 4);
-        o.vec8 = o.vec8 && fits(seg[i], width[i], elem, 8);
+        o.vec16 = o.vec16 && fits(seg[i], width[i], elem, 16 / elem);
     }
     o.a = a;
     o.b = b;

@@ -414,7 +414,8 @@ gdn_status gdn_mx_dequantize(int64_t rows, int32_t cols, const void* codes, cons
  *              will do then), 256-byte aligned; scratch only
  * A single row's strides are not read.  Any n_out and n_tok; n_in a multiple
  * of GDN_MX_GROUP up to GDN_MX_MAX_IN, ld_x up to twice that, and fewer than
- * 2^23 tiles of 64 tokens by 64 channels (UNSUPPORTED otherwise). */
+ * 2^22 tiles of 64 tokens by 64 channels (UNSUPPORTED otherwise).  Weights of
+ * 2^128 and more (scale bytes 253 and 254) may count as infinite. */
 #define GDN_MX_MAX_IN 1048576
 gdn_status gdn_mx_proj_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out, size_t* bytes);
 gdn_status gdn_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
