@@ -1,6 +1,7 @@
 // Projections with 4-bit weights: y = x W^T, x bf16, W in the format of
 // mx_format.hip, fp32 accumulation on the matrix cores.
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_common.h"
 #include "mfma_split.h"
@@ -20,6 +21,12 @@ using lds_ptr = __attribute__((address_space(3))) void*;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void* p, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, kRsrcWord3);
+}
+
+// 16 bytes per lane from base + offset + soffset straight into LDS, lane l's at
+// dst + 16 l.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rs, void* dst, int offset, int soffset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)dst, 16, offset, soffset, 0, 0);
 }
 
 // Where the output channels go: [0, end[0]) to seg[0], [end[0], end[1]) to
@@ -332,11 +339,11 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxO
 
 // Many tokens.  WT x WC waves, each 16 NT tokens x 16 NC channels, so a tile
 // of TT tokens x CC channels per workgroup; the input axis goes by in blocks
-// of 64 through three LDS stages, written by loads that store straight into
-// LDS two blocks ahead.  A stage holds the tokens' 128 bytes (64 bf16, or the
-// 64 hi and 64 lo bytes of the split) and the weights' 32 bytes of codes as
-// they are; scale bytes go through registers to a two-stage area ordered so
-// that a lane reads the scales of all its rows at once.
+// of 64 through STAGES stages of LDS, written by loads that store straight
+// into LDS.  A stage holds the tokens' 128 bytes (64 bf16, or the 64 hi and 64
+// lo bytes of the split) and the weights' 32 bytes of codes as they are; scale
+// bytes go through registers to a two-stage area ordered so that a lane reads
+// the scales of all its rows at once.
 //
 // bf16 (F8 false): lane q of MFMA j (16x16x32) takes k = 16 q + 8 j ..: one
 // 8-byte read of codes serves both MFMAs, expanded in registers.
@@ -345,21 +352,31 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxO
 // holds lane q's 32 codes for k = 32 q .., but 8-bit operands as k = 16 q ..
 // and 64 + 16 q ..; the scale of lane q is that of k = 32 q .. for both.
 //
-// A wave keeps its tokens' fragments of a block in registers and walks the
-// channels, so the next channels' codes arrive while the present ones
-// multiply; in the last step of a block each token fragment is replaced by the
-// next block's, and the barrier stands before that step, so no wave runs dry
-// at it.
-template <bool F8, int NT, int NC, int WT, int WC>
+// A wave keeps its tokens' fragments of a block in registers and takes its
+// channels in two halves, all of a half times one token fragment after the
+// other; the next half's codes arrive meanwhile.  The block's one barrier
+// stands between the halves.  It says that the next block has arrived and the
+// previous one's stage is free, to be filled with the block STAGES - 1 ahead.
+// Behind it the next block's token fragments are read, each as soon as the
+// second half is through with its predecessor, or where registers allow
+// (kDouble) all of them into a second set.
+template <bool F8, int NT, int NC, int WT, int WC, int STAGES>
 struct TileShape {
-    static constexpr int TT = 16 * NT * WT, CC = 16 * NC * WC, TH = 64 * WT * WC;
-    static constexpr int kX = TT * 128, kW = CC * 32, kStage = kX + kW;
-    static constexpr int kScale = 3 * kStage;            // two stages of CC * 2 + TT * 2 bytes
-    static constexpr int kBytes = kScale + 2 * 2 * (CC + TT);
-    static_assert(TT * 2 == TH && CC * 2 == TH, "per thread one scale byte of each operand, and 4 + 1 loads");
+    static constexpr int TT = 16 * NT * WT, CC = 16 * NC * WC, WAVES = WT * WC, TH = 64 * WAVES;
+    static constexpr int XL = TT / 8 / WAVES, WL = (CC / 32 + WAVES - 1) / WAVES;   // loads per wave and block
+    static constexpr int kX = TT * 128, kW = WL * WAVES * 1024, kStage = kX + kW;
+    static constexpr int NCP = (NC + 3) / 4 * 4, NTP = (NT + 3) / 4 * 4;            // scale bytes per lane
+    static constexpr int kWS = WC * 32 * NCP, kXS = WT * 32 * NTP;
+    static constexpr int kScale = STAGES * kStage, kBytes = kScale + 2 * (kWS + kXS);
+    // loads that may be in flight when the next block has to be there
+    static constexpr int kInFlight = (STAGES - 3) * (XL + WL + (F8 ? 2 : 1));
+    static constexpr int HC = NC / 2;
+    static constexpr bool kDouble = NT <= 2;
+    static_assert(TT % (8 * WAVES) == 0 && TT * 2 <= TH && CC * 2 <= TH, "whole loads; a scale byte per thread");
+    static_assert(NC % 2 == 0 && (STAGES == 3 || STAGES == 4) && kInFlight < 16, "the schedule");
     // the epilogue's rows (fp32, 16 bytes apart) in the stages
     static constexpr int kRow = 16 * NC * 4 + 16;
-    static_assert(WT * WC * 16 * kRow <= 3 * kStage, "epilogue rows fit");
+    static_assert(WAVES * 16 * kRow <= STAGES * kStage, "epilogue rows fit");
 };
 
 template <int OA, int OB>
@@ -376,7 +393,7 @@ __device__ __forceinline__ f32x4 mfma_f8(int ob, i32x8 w, i32x8 x, f32x4 c, int 
     }
 }
 // Byte oa of sw and ob of sx scale the operands (constants once unrolled).
-__device__ __forceinline__ f32x4 mfma_f8(int oa, int ob, i32x8 w, i32x8 x, f32x4 c, int sw, int sx) {
+[[maybe_unused]] __device__ __forceinline__ f32x4 mfma_f8(int oa, int ob, i32x8 w, i32x8 x, f32x4 c, int sw, int sx) {
     switch (oa) {
         case 0: return mfma_f8<0>(ob, w, x, c, sw, sx);
         case 1: return mfma_f8<1>(ob, w, x, c, sw, sx);
@@ -401,10 +418,10 @@ __device__ __forceinline__ float mx_dot(const MxIn& p, int64_t t, int n) {
     return y;
 }
 
-template <typename T, bool F8, int NT, int NC, int WT, int WC>
+template <typename T, bool F8, int NT, int NC, int WT, int WC, int STAGES>
 __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut o, MxSplit sp, int tiles_t,
                                                                   int n_end) {
-    using S = TileShape<F8, NT, NC, WT, WC>;
+    using S = TileShape<F8, NT, NC, WT, WC, STAGES>;
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -424,15 +441,18 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
     // eight rows of tokens or 32 rows of weights.  Slot s of a token row holds
     // chunk s ^ (row / 2) % 8, of a weight row s ^ (row / 8) % 2, so the 16
     // rows of a fragment read spread over all banks.
-    int gx[4], xchunk[4];
+    int gx[S::XL], xchunk[S::XL], gw[S::WL];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = wave * 32 + i * 8 + (lane >> 3);
+    for (int i = 0; i < S::XL; ++i) {
+        const int r = (wave * S::XL + i) * 8 + (lane >> 3);
         xchunk[i] = (lane & 7) ^ ((r >> 1) & 7);
         gx[i] = offset_if(r < toks, (F8 ? r * sp.row : (int)(r * p.ld_x * 2)) + xchunk[i] * 16);
     }
-    const int wrow = wave * 32 + (lane >> 1), wchunk = (lane & 1) ^ ((wrow >> 3) & 1);
-    const int gw = offset_if(wrow < rows, wrow * half + wchunk * 16);
+#pragma unroll
+    for (int i = 0; i < S::WL; ++i) {
+        const int r = (wave * S::WL + i) * 32 + (lane >> 1);
+        gw[i] = offset_if(r < rows, r * half + ((lane & 1) ^ ((r >> 3) & 1)) * 16);
+    }
     // Past a row's end the tokens are zeros (or the split's padding) and the
     // scales 0, so the codes there may be anything; past the last block it is
     // loaded again and not used.  Scalar offsets stay inside the descriptors:
@@ -441,29 +461,32 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
         const int kb = min(k, blocks - 1);
         uint8_t* base = lds + st * S::kStage;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                x_rs, (lds_ptr)(base + (wave * 4 + i) * 1024), 16,
-                F8 ? gx[i] : offset_if(kb * 64 + xchunk[i] * 8 < p.n_in, gx[i]), kb * 128, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rs, (lds_ptr)(base + S::kX + wave * 1024), 16, gw, kb * 32, 0, 0);
+        for (int i = 0; i < S::XL; ++i)
+            load_lds16(x_rs, base + (wave * S::XL + i) * 1024,
+                       F8 ? gx[i] : offset_if(kb * 64 + xchunk[i] * 8 < p.n_in, gx[i]), kb * 128);
+#pragma unroll
+        for (int i = 0; i < S::WL; ++i)
+            load_lds16(w_rs, base + S::kX + (wave * S::WL + i) * 1024, gw[i], kb * 32);
     };
     // Scale bytes: thread tid carries group tid % 2 of row tid / 2.
     const int srow = tid >> 1, sgrp = tid & 1;
-    uint32_t sw_in, sx_in = 0;
-    const auto issue_scales = [&](int kb) {
+    uint32_t sw_in[2], sx_in[2];
+    const auto issue_scales = [&](int kb, int r) {
         const int g = kb * 2 + sgrp;
-        sw_in = __builtin_amdgcn_raw_buffer_load_b8(
+        sw_in[r] = __builtin_amdgcn_raw_buffer_load_b8(
             s_rs, offset_if((srow < rows) & (g < groups), srow * groups + g), 0, 0);
         if constexpr (F8)
-            sx_in = __builtin_amdgcn_raw_buffer_load_b8(
+            sx_in[r] = __builtin_amdgcn_raw_buffer_load_b8(
                 e_rs, offset_if((srow < toks) & (kb < blocks), srow * (sp.row / 64) + g), 0, 0);
+        __builtin_amdgcn_sched_barrier(0);   // before the block's other loads: the waits count on it
     };
-    const int sw_at = ((srow / (16 * NC) * 16 + (srow & 15)) * 2 + sgrp) * NC + (srow >> 4) % NC;
-    const int sx_at = 2 * S::CC + ((srow / (16 * NT) * 16 + (srow & 15)) * 2 + sgrp) * NT + (srow >> 4) % NT;
-    const auto put_scales = [&](int kb) {
-        uint8_t* base = lds + S::kScale + (kb & 1) * (2 * (S::CC + S::TT));
-        base[sw_at] = (uint8_t)sw_in;
-        if constexpr (F8) base[sx_at] = (uint8_t)sx_in;
+    const int sw_at = ((srow / (16 * NC) * 16 + (srow & 15)) * 2 + sgrp) * S::NCP + (srow >> 4) % NC;
+    const int sx_at = S::kWS + ((srow / (16 * NT) * 16 + (srow & 15)) * 2 + sgrp) * S::NTP + (srow >> 4) % NT;
+    const auto put_scales = [&](int kb, int r) {
+        uint8_t* base = lds + S::kScale + (kb & 1) * (S::kWS + S::kXS);
+        if (S::CC * 2 == S::TH || srow < S::CC) base[sw_at] = (uint8_t)sw_in[r];
+        if constexpr (F8)
+            if (S::TT * 2 == S::TH || srow < S::TT) base[sx_at] = (uint8_t)sx_in[r];
     };
 
     // Fragment reads.
@@ -472,24 +495,27 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
     const int xr = (wt * 16 * NT + m) * 128, xo0 = xr + 16 * (xc0 ^ xkey), xo1 = xr + 16 * (xc1 ^ xkey);
     const int wo = S::kX + (wc * 16 * NC + m) * 32 +
                    (F8 ? 16 * ((q & 1) ^ wkey) : 16 * ((q >> 1) ^ wkey) + 8 * (q & 1));
-    const int swo = ((wc * 16 + m) * 2 + (F8 ? q & 1 : q >> 1)) * NC;
-    const int sxo = 2 * S::CC + ((wt * 16 + m) * 2 + (q & 1)) * NT;
-    u32x4 xf[NT][2];
+    const int swo = ((wc * 16 + m) * 2 + (F8 ? q & 1 : q >> 1)) * S::NCP;
+    const int sxo = S::kWS + ((wt * 16 + m) * 2 + (q & 1)) * S::NTP;
+    u32x4 xf[S::kDouble ? 2 : 1][NT][2];
     using Codes = std::conditional_t<F8, u32x4, u32x2>;
-    Codes wf[2];
-    uint32_t sw[2][NC / 4], sx[2];
-    const auto read_x = [&](int st, int t) {
+    Codes wf[2][S::HC];
+    bf16x8 we[F8 ? 1 : S::HC][2];   // a half's weights, expanded
+    uint32_t sw[2][S::NCP / 4], sx[2];
+    const auto read_x = [&](int st, int t, int to) {
         const uint8_t* base = lds + st * S::kStage + t * 2048;
-        xf[t][0] = *reinterpret_cast<const u32x4*>(base + xo0);
-        xf[t][1] = *reinterpret_cast<const u32x4*>(base + xo1);
+        xf[to][t][0] = *reinterpret_cast<const u32x4*>(base + xo0);
+        xf[to][t][1] = *reinterpret_cast<const u32x4*>(base + xo1);
     };
-    const auto read_w = [&](int st, int c, Codes& w) {
-        w = *reinterpret_cast<const Codes*>(lds + st * S::kStage + c * 512 + wo);
+    const auto read_w = [&](int st, int h) {
+#pragma unroll
+        for (int i = 0; i < S::HC; ++i)
+            wf[h][i] = *reinterpret_cast<const Codes*>(lds + st * S::kStage + (h * S::HC + i) * 512 + wo);
     };
     const auto read_scales = [&](int kb, int to) {
-        const uint8_t* base = lds + S::kScale + (kb & 1) * (2 * (S::CC + S::TT));
+        const uint8_t* base = lds + S::kScale + (kb & 1) * (S::kWS + S::kXS);
 #pragma unroll
-        for (int i = 0; i < NC / 4; ++i) sw[to][i] = *reinterpret_cast<const uint32_t*>(base + swo + 4 * i);
+        for (int i = 0; i < S::NCP / 4; ++i) sw[to][i] = *reinterpret_cast<const uint32_t*>(base + swo + 4 * i);
         if constexpr (F8) sx[to] = *reinterpret_cast<const uint32_t*>(base + sxo) - (q >> 1) * 0x05050505u;
     };
     f32x4 acc[NT][NC];
@@ -498,73 +524,94 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const auto barrier = [&](int kb) {
-        // every wave's loads of block kb are done, and its reads of block kb - 1
-        // (the last of them before this point)
-        __builtin_amdgcn_s_waitcnt(0x0f75);                      // vmcnt(5): one block's loads in flight
-        put_scales(kb);
-        __builtin_amdgcn_s_waitcnt(0xc07f);                      // lgkmcnt(0)
-        asm volatile("s_barrier" ::: "memory");
-    };
-    issue_scales(0);
-    __builtin_amdgcn_sched_barrier(0);
+    constexpr int kVm = 0x0f70, kLgkm0 = 0xc07f;   // wait for all but the low bits' vector loads; for all of LDS
+    issue_scales(0, 0);
     issue(0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    // scale bytes of block kb go through register kb % 2 with four stages; with
+    // three the next ones are loaded when these have been put down
+    if constexpr (STAGES == 4) issue_scales(1, 1);
     issue(1, 1);
-    barrier(0);
-    issue_scales(1);
-    __builtin_amdgcn_sched_barrier(0);   // the scales' loads come first: the wait counts on it
-    issue(2, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(kVm | (S::XL + S::WL + (STAGES == 4 ? F8 ? 2 : 1 : 0)));
+    put_scales(0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    issue_scales(STAGES - 2, 0);
+    if constexpr (STAGES == 4) issue(2, 2);
+    __builtin_amdgcn_s_waitcnt(kLgkm0);
+    asm volatile("s_barrier" ::: "memory");
 #pragma unroll
-    for (int t = 0; t < NT; ++t) read_x(0, t);
-    read_w(0, 0, wf[0]);
+    for (int t = 0; t < NT; ++t) read_x(0, t, 0);
+    read_w(0, 0);
     read_scales(0, 0);
 
     int st = 0;
-    for (int kb = 0; kb < blocks; ++kb) {
-        const int nx = st == 2 ? 0 : st + 1;
+    // P is kb % 2 where registers are held twice (a constant once inlined), else 0
+    const auto block = [&](int kb, const int P) __attribute__((always_inline)) {
+        const int N = S::kDouble ? 1 - P : 0;
+        const int nx = st + 1 == STAGES ? 0 : st + 1;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            if (c == NC - 1) {
-                barrier(kb + 1);
-                issue_scales(kb + 2);
+        for (int h = 0; h < 2; ++h) {
+            if (h == 1) {
+                __builtin_amdgcn_s_waitcnt(kVm | S::kInFlight);
+                put_scales(kb + 1, STAGES == 3 ? 0 : 1 - P);
+                __builtin_amdgcn_s_waitcnt(kLgkm0);
+                asm volatile("s_barrier" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
-                issue(kb + 3, st);
-                read_w(nx, 0, wf[(c + 1) & 1]);
-                read_scales(kb + 1, 1);
+                read_w(nx, 0);
+                read_scales(kb + 1, 1 - P);
+                if constexpr (S::kDouble)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) read_x(nx, t, N);
+                issue_scales(kb + STAGES - 1, STAGES == 3 ? 0 : 1 - P);
+                issue(kb + STAGES - 1, st == 0 ? STAGES - 1 : st - 1);
             } else {
-                read_w(st, c + 1, wf[(c + 1) & 1]);
+                read_w(st, 1);
             }
-            if constexpr (F8) {
-                const Codes& w = wf[c & 1];
-                const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const u32x4 h = xf[t][0], l = xf[t][1];
-                    const i32x8 b = {(int)h[0], (int)h[1], (int)h[2], (int)h[3],
-                                     (int)l[0], (int)l[1], (int)l[2], (int)l[3]};
-                    acc[t][c] = mfma_f8(c & 3, t & 3, a, b, acc[t][c], (int)sw[0][c / 4], (int)sx[0]);
-                    if (c == NC - 1) read_x(nx, t);
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int i = 0; i < S::HC; ++i) {
+                    const int c = h * S::HC + i;
+                    const Codes w = wf[h][i];
+                    if constexpr (F8) {
+                        const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+                        const u32x4 hi = xf[P][t][0], lo = xf[P][t][1];
+                        const i32x8 b = {(int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3],
+                                         (int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3]};
+                        acc[t][c] = mfma_f8(c & 3, t & 3, a, b, acc[t][c], (int)sw[P][c / 4], (int)sx[P]);
+                    } else {
+                        if (t == 0) {
+                            const float scale = __uint_as_float((sw[P][c / 4] >> (8 * (c & 3)) & 0xffu) << 23);
+                            we[i][0] = mx_expand(w[0], scale);
+                            we[i][1] = mx_expand(w[1], scale);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                we[i][j], __builtin_bit_cast(bf16x8, xf[P][t][j]), acc[t][c], 0, 0, 0);
+                    }
                 }
-            } else {
-                const Codes w = wf[c & 1];
-                const float scale = __uint_as_float((sw[0][c / 4] >> (8 * (c & 3)) & 0xffu) << 23);
-                const bf16x8 w0 = mx_expand(w[0], scale), w1 = mx_expand(w[1], scale);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        w0, __builtin_bit_cast(bf16x8, xf[t][0]), acc[t][c], 0, 0, 0);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        w1, __builtin_bit_cast(bf16x8, xf[t][1]), acc[t][c], 0, 0, 0);
-                    if (c == NC - 1) read_x(nx, t);
-                }
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (!S::kDouble)
+                    if (h == 1) read_x(nx, t, 0);
             }
         }
+        if constexpr (!S::kDouble) {
 #pragma unroll
-        for (int i = 0; i < NC / 4; ++i) sw[0][i] = sw[1][i];
-        sx[0] = sx[1];
+            for (int i = 0; i < S::NCP / 4; ++i) sw[0][i] = sw[1][i];
+            sx[0] = sx[1];
+        }
         st = nx;
+    };
+    if constexpr (S::kDouble) {
+        for (int kb = 0; kb < blocks; kb += 2) {
+            block(kb, 0);
+            if (kb + 1 == blocks) break;
+            block(kb + 1, 1);
+        }
+    } else {
+        for (int kb = 0; kb < blocks; ++kb) block(kb, 0);
     }
     // the loads past the last block are done before their stages are used again
     __builtin_amdgcn_s_waitcnt(0x0070);                          // vmcnt(0) lgkmcnt(0)
@@ -653,16 +700,30 @@ hipError_t split(const MxIn& p, const MxOut& o, int c0, const MxSplit& sp, hipSt
     return hipGetLastError();
 }
 
-template <typename T, bool F8, int NT, int NC, int WT, int WC>
+template <typename T, bool F8, int NT, int NC, int WT, int WC, int STAGES>
 hipError_t tile(const MxIn& p, const MxOut& o, const MxSplit& sp, int n_end, hipStream_t stream) {
-    using S = TileShape<F8, NT, NC, WT, WC>;
+    using S = TileShape<F8, NT, NC, WT, WC, STAGES>;
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_dynamic_lds(&mx_tile_kernel<T, F8, NT, NC, WT, WC>, S::kBytes, &done);
+    const hipError_t e = allow_dynamic_lds(&mx_tile_kernel<T, F8, NT, NC, WT, WC, STAGES>, S::kBytes, &done);
     if (e != hipSuccess) return e;
     const int tiles_t = (int)((p.n_tok + S::TT - 1) / S::TT), tiles_c = (n_end + S::CC - 1) / S::CC;
-    hipLaunchKernelGGL((mx_tile_kernel<T, F8, NT, NC, WT, WC>), dim3((unsigned)tiles_t * tiles_c), dim3(S::TH),
+    hipLaunchKernelGGL((mx_tile_kernel<T, F8, NT, NC, WT, WC, STAGES>), dim3((unsigned)tiles_t * tiles_c), dim3(S::TH),
                        S::kBytes, stream, p, o, sp, tiles_t, n_end);
     return hipGetLastError();
+}
+
+// The tile shape whose rounds of workgroups take the least: the measure is the
+// tile's area times the rounds.
+template <typename T, bool F8>
+hipError_t launch_tiles(const MxIn& p, const MxOut& o, const MxSplit& sp, int n_end, hipStream_t stream) {
+    const auto cost = [&](int tt, int cc) {
+        const int64_t tiles = ((p.n_tok + tt - 1) / tt) * ((n_end + cc - 1) / cc);
+        return (tiles + 255) / 256 * tt * cc;
+    };
+    const int64_t large = cost(256, 256), mid = cost(128, 192), small = cost(128, 128);
+    if (large <= mid && large <= small) return tile<T, F8, 4, 8, 4, 2, 3>(p, o, sp, n_end, stream);
+    if (mid <= small) return tile<T, F8, 2, 6, 4, 2, 4>(p, o, sp, n_end, stream);
+    return tile<T, F8, 2, 4, 4, 2, 4>(p, o, sp, n_end, stream);
 }
 
 constexpr int64_t kSkinnyTokens = 64;   // up to here the skinny kernel takes all channels
@@ -713,7 +774,6 @@ hipError_t launch_few(const MxIn& p, const MxOut& o, hipStream_t stream) {
 template <typename T>
 hipError_t launch_typed(const MxIn& p, const MxOut& o, void* workspace, hipStream_t stream) {
     if (p.n_tok <= kSkinnyTokens && p.n_in >= 128) return launch_few<T>(p, o, stream);
-    const bool large = ((p.n_tok + 255) / 256) * ((p.n_out + 255) / 256) >= 256;
     if constexpr (sizeof(T) == 2) {
         if (use_split(p.n_tok, p.n_in, GDN_BF16)) {
             size_t bytes;
@@ -721,13 +781,11 @@ hipError_t launch_typed(const MxIn& p, const MxOut& o, void* workspace, hipStrea
             const int n_end = o.end[3];
             const hipError_t e = split(p, o, n_end, sp, stream);
             if (e != hipSuccess) return e;
-            return large ? tile<T, true, 4, 8, 4, 2>(p, o, sp, n_end, stream)
-                         : tile<T, true, 4, 4, 2, 2>(p, o, sp, n_end, stream);
+            return launch_tiles<T, true>(p, o, sp, n_end, stream);
         }
     }
     const MxSplit none{};
-    return large ? tile<T, false, 4, 8, 4, 2>(p, o, none, p.n_out, stream)
-                 : tile<T, false, 4, 4, 2, 2>(p, o, none, p.n_out, stream);
+    return launch_tiles<T, false>(p, o, none, p.n_out, stream);
 }
 
 }  // namespace
