@@ -123,11 +123,14 @@ struct MxIn {
 // is at most half of its last of four bits, a multiple of x's own last bit and
 // so exact in lo: values down to 2^-14 of the largest are split without error,
 // and smaller ones to within 2^-22 of the largest.
+// Blocks of 64 values lie token by token, so that a tile's share of a block is
+// one piece of memory: rows a power of two apart would all come from the same
+// few channels of the cache.
 struct MxSplit {
-    uint8_t* data;     // [n_tok][row]: per 64 values 64 hi bytes, then 64 lo bytes
-    uint8_t* scales;   // [n_tok][row / 64], one byte per 32 values; 255: not all finite
+    uint8_t* data;     // [2 pairs][n_tok][128]: 64 hi bytes, then 64 lo bytes
+    uint8_t* scales;   // [pairs][n_tok][4], one byte per 32 values; 255: not all finite
     uint8_t* flags;    // [n_tok]: bit 0 an infinity, bit 1 a NaN
-    int row;           // bytes of a token's data, a multiple of 128
+    int pairs;         // of blocks, the last padded with zeros
 };
 
 // The four codes' dwords of four lanes 16 apart, transposed: lane row q gets
@@ -283,7 +286,7 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxO
                                                           c0 + (int)(blockIdx.x % cols) * (16 * kGateChannels));
         return;
     }
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, values = sp.row / 2;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, values = sp.pairs * 128;
     const int64_t stride = (int64_t)(gridDim.x - gate_wgs) * kSkinnyWaves;
     for (int64_t t = (int64_t)(blockIdx.x - gate_wgs) * kSkinnyWaves + wave; t < p.n_tok; t += stride) {
         const uint16_t* x = p.x + t * p.ld_x;
@@ -324,11 +327,11 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxO
                 else { hi[i / 2] = (uint32_t)h & 0xffffu; lo[i / 2] = (uint32_t)l & 0xffffu; }
             }
             if (v < values) {
-                uint8_t* d = sp.data + t * sp.row + (v >> 6) * 128 + (v & 63);
+                uint8_t* d = sp.data + ((v >> 6) * p.n_tok + t) * 128 + (v & 63);
                 const u32x4 zero = {0, 0, 0, 0};
                 *reinterpret_cast<u32x4*>(d) = finite ? hi : zero;
                 *reinterpret_cast<u32x4*>(d + 64) = finite ? lo : zero;
-                if ((lane & 1) == 0) sp.scales[t * (sp.row / 64) + (v >> 5)] = (uint8_t)(finite ? s : 255);
+                if ((lane & 1) == 0) sp.scales[((v >> 7) * p.n_tok + t) * 4 + (v >> 5 & 3)] = (uint8_t)(finite ? s : 255);
             }
             flag |= finite ? 0u : top > 0x7f800000u ? 2u : 1u;
         }
@@ -337,13 +340,15 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxO
     }
 }
 
-// Many tokens.  WT x WC waves, each 16 NT tokens x 16 NC channels, so a tile
-// of TT tokens x CC channels per workgroup; the input axis goes by in blocks
-// of 64 through STAGES stages of LDS, written by loads that store straight
-// into LDS.  A stage holds the tokens' 128 bytes (64 bf16, or the 64 hi and 64
-// lo bytes of the split) and the weights' 32 bytes of codes as they are; scale
-// bytes go through registers to a two-stage area ordered so that a lane reads
-// the scales of all its rows at once.
+// Many tokens.  Eight waves, WT x WC, each 16 NT tokens x 16 NC channels, so a
+// tile of TT tokens x CC channels per workgroup.  The input axis goes by in
+// blocks of 64 through LDS, written by loads that store straight into LDS: the
+// tokens' 128 bytes of a block (64 bf16, or the 64 hi and 64 lo bytes of the
+// split) through STAGES stages, the weights' 64 bytes of a pair of blocks,
+// codes as they are, through STAGES - 1.  The four scale bytes of a pair go
+// through a register to a two-stage area ordered so that a lane reads those of
+// its rows side by side.  What bounds the kernel is this feed, not the matrix
+// units, so each load takes as much of a row at once as LDS holds.
 //
 // bf16 (F8 false): lane q of MFMA j (16x16x32) takes k = 16 q + 8 j ..: one
 // 8-byte read of codes serves both MFMAs, expanded in registers.
@@ -363,43 +368,25 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxO
 template <bool F8, int NT, int NC, int WT, int WC, int STAGES>
 struct TileShape {
     static constexpr int TT = 16 * NT * WT, CC = 16 * NC * WC, WAVES = WT * WC, TH = 64 * WAVES;
-    static constexpr int XL = TT / 8 / WAVES, WL = (CC / 32 + WAVES - 1) / WAVES;   // loads per wave and block
-    static constexpr int kX = TT * 128, kW = WL * WAVES * 1024, kStage = kX + kW;
-    static constexpr int NCP = (NC + 3) / 4 * 4, NTP = (NT + 3) / 4 * 4;            // scale bytes per lane
-    static constexpr int kWS = WC * 32 * NCP, kXS = WT * 32 * NTP;
-    static constexpr int kScale = STAGES * kStage, kBytes = kScale + 2 * (kWS + kXS);
-    // loads that may be in flight when the next block has to be there
-    static constexpr int kInFlight = (STAGES - 3) * (XL + WL + (F8 ? 2 : 1));
-    static constexpr int HC = NC / 2;
+    static constexpr int XL = TT / 8 / WAVES;                      // loads per wave and block
+    static constexpr int WL = (CC / 16 + WAVES - 1) / WAVES;       // loads per wave and pair
+    static constexpr int WB = STAGES - 1;
+    static constexpr int kX = TT * 128, kW = WL * WAVES * 1024, kWeights = STAGES * kX;
+    static constexpr int HC = NC / 2, HP = HC <= 2 ? 2 : 4;        // channels of a half; their scale words' places
+    static constexpr int kWS = WC * 16 * 2 * HP * 4, kXS = WT * 16 * NT * 4;
+    static constexpr int kScale = kWeights + WB * kW, kBytes = kScale + 2 * (kWS + kXS);
     static constexpr bool kDouble = NT <= 2;
-    static_assert(TT % (8 * WAVES) == 0 && TT * 2 <= TH && CC * 2 <= TH, "whole loads; a scale byte per thread");
-    static_assert(NC % 2 == 0 && (STAGES == 3 || STAGES == 4) && kInFlight < 16, "the schedule");
+    static_assert(TH == 512 && TT <= 256 && CC <= 256 && TT % (8 * WAVES) == 0, "a scale word per thread; whole loads");
+    static_assert(NC % 2 == 0 && (STAGES == 3 || STAGES == 4) && XL + WL < 16, "the schedule");
     // the epilogue's rows (fp32, 16 bytes apart) in the stages
     static constexpr int kRow = 16 * NC * 4 + 16;
-    static_assert(WAVES * 16 * kRow <= STAGES * kStage, "epilogue rows fit");
+    static_assert(WAVES * 16 * kRow <= kScale && kBytes <= 160 * 1024, "fits");
 };
 
-template <int OA, int OB>
-__device__ __forceinline__ f32x4 mfma_f8(i32x8 w, i32x8 x, f32x4 c, int sw, int sx) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 4, 0, OA, sw, OB, sx);
-}
-template <int OA>
-__device__ __forceinline__ f32x4 mfma_f8(int ob, i32x8 w, i32x8 x, f32x4 c, int sw, int sx) {
-    switch (ob) {
-        case 0: return mfma_f8<OA, 0>(w, x, c, sw, sx);
-        case 1: return mfma_f8<OA, 1>(w, x, c, sw, sx);
-        case 2: return mfma_f8<OA, 2>(w, x, c, sw, sx);
-        default: return mfma_f8<OA, 3>(w, x, c, sw, sx);
-    }
-}
-// Byte oa of sw and ob of sx scale the operands (constants once unrolled).
-[[maybe_unused]] __device__ __forceinline__ f32x4 mfma_f8(int oa, int ob, i32x8 w, i32x8 x, f32x4 c, int sw, int sx) {
-    switch (oa) {
-        case 0: return mfma_f8<0>(ob, w, x, c, sw, sx);
-        case 1: return mfma_f8<1>(ob, w, x, c, sw, sx);
-        case 2: return mfma_f8<2>(ob, w, x, c, sw, sx);
-        default: return mfma_f8<3>(ob, w, x, c, sw, sx);
-    }
+// Byte 2 p of sw and of sx scale the operands (p a constant once inlined).
+__device__ __forceinline__ f32x4 mfma_f8(int p, i32x8 w, i32x8 x, f32x4 c, int sw, int sx) {
+    return p ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 4, 0, 2, sw, 2, sx)
+             : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 4, 0, 0, sw, 0, sx);
 }
 
 // One output by the definition, for tokens that hold an infinity.
@@ -430,93 +417,110 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
     const int64_t t0 = (int64_t)(blockIdx.x % tiles_t) * S::TT;
     const int n0 = (int)(blockIdx.x / tiles_t) * S::CC;
     const int toks = (int)min((int64_t)S::TT, p.n_tok - t0), rows = min(S::CC, n_end - n0);
-    const int half = p.n_in / 2, groups = p.n_in / 32, blocks = (groups + 1) / 2;
-    const void* xp = F8 ? static_cast<const void*>(sp.data + t0 * sp.row) : p.x + t0 * p.ld_x;
-    const auto x_rs = buf_rsrc(xp, F8 ? (int64_t)toks * sp.row : ((toks - 1) * p.ld_x + p.n_in) * 2);
+    const int half = p.n_in / 2, groups = p.n_in / 32, blocks = (groups + 1) / 2, pairs = (groups + 3) / 4;
+    const auto x_rs = buf_rsrc(F8 ? nullptr : p.x + t0 * p.ld_x, ((toks - 1) * p.ld_x + p.n_in) * 2);
     const auto w_rs = buf_rsrc(p.codes + (int64_t)n0 * half, (int64_t)rows * half);
-    const auto s_rs = buf_rsrc(p.scales + (int64_t)n0 * groups, (int64_t)rows * groups);
-    const auto e_rs = buf_rsrc(F8 ? sp.scales + t0 * (sp.row / 64) : sp.scales, F8 ? (int64_t)toks * (sp.row / 64) : 0);
 
     // Loads into LDS: lane l of a wave's load writes 16 bytes at 16 l, i.e.
-    // eight rows of tokens or 32 rows of weights.  Slot s of a token row holds
-    // chunk s ^ (row / 2) % 8, of a weight row s ^ (row / 8) % 2, so the 16
+    // eight rows of tokens or 16 rows of weights.  Slot s of a token row holds
+    // chunk s ^ (row / 2) % 8, of a weight row s ^ (row / 4) % 4, so the 16
     // rows of a fragment read spread over all banks.
     int gx[S::XL], xchunk[S::XL], gw[S::WL];
 #pragma unroll
     for (int i = 0; i < S::XL; ++i) {
         const int r = (wave * S::XL + i) * 8 + (lane >> 3);
         xchunk[i] = (lane & 7) ^ ((r >> 1) & 7);
-        gx[i] = offset_if(r < toks, (F8 ? r * sp.row : (int)(r * p.ld_x * 2)) + xchunk[i] * 16);
+        gx[i] = offset_if(r < toks, (F8 ? r * 128 : (int)(r * p.ld_x * 2)) + xchunk[i] * 16);
     }
 #pragma unroll
     for (int i = 0; i < S::WL; ++i) {
-        const int r = (wave * S::WL + i) * 32 + (lane >> 1);
-        gw[i] = offset_if(r < rows, r * half + ((lane & 1) ^ ((r >> 3) & 1)) * 16);
+        const int r = (wave * S::WL + i) * 16 + (lane >> 2);
+        gw[i] = offset_if(r < rows, r * half + ((lane & 3) ^ ((r >> 2) & 3)) * 16);
     }
     // Past a row's end the tokens are zeros (or the split's padding) and the
     // scales 0, so the codes there may be anything; past the last block it is
     // loaded again and not used.  Scalar offsets stay inside the descriptors:
     // their range is checked on what is left behind that offset.
-    const auto issue = [&](int k, int st) {
+    const auto issue_x = [&](int k, int st) {
         const int kb = min(k, blocks - 1);
-        uint8_t* base = lds + st * S::kStage;
+        const auto rs = F8 ? buf_rsrc(sp.data + (kb * p.n_tok + t0) * 128, toks * 128) : x_rs;
 #pragma unroll
         for (int i = 0; i < S::XL; ++i)
-            load_lds16(x_rs, base + (wave * S::XL + i) * 1024,
-                       F8 ? gx[i] : offset_if(kb * 64 + xchunk[i] * 8 < p.n_in, gx[i]), kb * 128);
+            load_lds16(rs, lds + st * S::kX + (wave * S::XL + i) * 1024,
+                       F8 ? gx[i] : offset_if(kb * 64 + xchunk[i] * 8 < p.n_in, gx[i]), F8 ? 0 : kb * 128);
+    };
+    const auto issue_w = [&](int k, int wb) {
 #pragma unroll
         for (int i = 0; i < S::WL; ++i)
-            load_lds16(w_rs, base + S::kX + (wave * S::WL + i) * 1024, gw[i], kb * 32);
+            load_lds16(w_rs, lds + S::kWeights + wb * S::kW + (wave * S::WL + i) * 1024, gw[i],
+                       min(k, pairs - 1) * 64);
     };
-    // Scale bytes: thread tid carries group tid % 2 of row tid / 2.
-    const int srow = tid >> 1, sgrp = tid & 1;
-    uint32_t sw_in[2], sx_in[2];
-    const auto issue_scales = [&](int kb, int r) {
-        const int g = kb * 2 + sgrp;
-        sw_in[r] = __builtin_amdgcn_raw_buffer_load_b8(
-            s_rs, offset_if((srow < rows) & (g < groups), srow * groups + g), 0, 0);
-        if constexpr (F8)
-            sx_in[r] = __builtin_amdgcn_raw_buffer_load_b8(
-                e_rs, offset_if((srow < toks) & (kb < blocks), srow * (sp.row / 64) + g), 0, 0);
-        __builtin_amdgcn_sched_barrier(0);   // before the block's other loads: the waits count on it
+    // Scale words: the first half of the threads carries a weight row's each, the
+    // other a token's.  A weight row's word may be unaligned; where the row ends
+    // inside it, it starts earlier, by past() bytes that are shifted out.
+    const bool of_x = wave >= 4;
+    const int srow = tid & 255;
+    const uint8_t* s_at = of_x ? sp.scales + (t0 + min(srow, toks - 1)) * 4
+                               : p.scales + (int64_t)(n0 + min(srow, rows - 1)) * groups;
+    const int64_t s_step = of_x ? p.n_tok * 4 : 4;
+    const auto past = [&](int kp) { return of_x ? 0 : max(0, kp * 4 + 4 - groups); };
+    uint32_t s_in = 0;
+    const auto issue_scales = [&](int k) {
+        const int kp = min(k, pairs - 1);
+        if (F8 || !of_x) {
+            if (groups >= 4) {
+                __builtin_memcpy(&s_in, s_at + kp * s_step - past(kp), 4);
+            } else {
+                s_in = 0;
+#pragma unroll 1
+                for (int j = 0; j < groups; ++j) s_in |= (uint32_t)s_at[j] << (8 * j);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);   // before the pair's other loads: the waits count on it
     };
-    const int sw_at = ((srow / (16 * NC) * 16 + (srow & 15)) * 2 + sgrp) * S::NCP + (srow >> 4) % NC;
-    const int sx_at = S::kWS + ((srow / (16 * NT) * 16 + (srow & 15)) * 2 + sgrp) * S::NTP + (srow >> 4) % NT;
-    const auto put_scales = [&](int kb, int r) {
-        uint8_t* base = lds + S::kScale + (kb & 1) * (S::kWS + S::kXS);
-        if (S::CC * 2 == S::TH || srow < S::CC) base[sw_at] = (uint8_t)sw_in[r];
-        if constexpr (F8)
-            if (S::TT * 2 == S::TH || srow < S::TT) base[sx_at] = (uint8_t)sx_in[r];
+    const int rr = srow >> 4;
+    const int s_to = of_x ? S::kWS + ((rr / NT * 16 + (srow & 15)) * NT + rr % NT) * 4
+                          : ((rr / NC * 16 + (srow & 15)) * 2 * S::HP + rr % NC / S::HC * S::HP + rr % NC % S::HC) * 4;
+    const auto put_scales = [&](int kp) {
+        if (srow < (of_x ? F8 ? S::TT : 0 : S::CC))
+            *reinterpret_cast<uint32_t*>(lds + S::kScale + (kp & 1) * (S::kWS + S::kXS) + s_to) =
+                groups >= 4 ? s_in >> (8 * past(min(kp, pairs - 1))) : s_in;
     };
 
-    // Fragment reads.
-    const int xkey = (m >> 1) & 7, wkey = (m >> 3) & 1;
+    // Fragment reads; b is the block's place in its pair.
+    const int xkey = (m >> 1) & 7, wkey = (m >> 2) & 3;
     const int xc0 = F8 ? q : 2 * q, xc1 = F8 ? 4 + q : 2 * q + 1;
     const int xr = (wt * 16 * NT + m) * 128, xo0 = xr + 16 * (xc0 ^ xkey), xo1 = xr + 16 * (xc1 ^ xkey);
-    const int wo = S::kX + (wc * 16 * NC + m) * 32 +
-                   (F8 ? 16 * ((q & 1) ^ wkey) : 16 * ((q >> 1) ^ wkey) + 8 * (q & 1));
-    const int swo = ((wc * 16 + m) * 2 + (F8 ? q & 1 : q >> 1)) * S::NCP;
-    const int sxo = S::kWS + ((wt * 16 + m) * 2 + (q & 1)) * S::NTP;
+    const int wr = S::kWeights + (wc * 16 * NC + m) * 64;
+    const int wo0 = wr + (F8 ? 16 * ((q & 1) ^ wkey) : 16 * ((q >> 1) ^ wkey) + 8 * (q & 1)), wo1 = wo0 ^ 32;
+    const int s_shift = 8 * (F8 ? q & 1 : q >> 1);
     u32x4 xf[S::kDouble ? 2 : 1][NT][2];
     using Codes = std::conditional_t<F8, u32x4, u32x2>;
     Codes wf[2][S::HC];
     bf16x8 we[F8 ? 1 : S::HC][2];   // a half's weights, expanded
-    uint32_t sw[2][S::NCP / 4], sx[2];
+    uint32_t sw[2][S::HC], sx[2][NT];
     const auto read_x = [&](int st, int t, int to) {
-        const uint8_t* base = lds + st * S::kStage + t * 2048;
+        const uint8_t* base = lds + st * S::kX + t * 2048;
         xf[to][t][0] = *reinterpret_cast<const u32x4*>(base + xo0);
         xf[to][t][1] = *reinterpret_cast<const u32x4*>(base + xo1);
     };
-    const auto read_w = [&](int st, int h) {
+    const auto read_w = [&](int wb, int b, int h) {
 #pragma unroll
         for (int i = 0; i < S::HC; ++i)
-            wf[h][i] = *reinterpret_cast<const Codes*>(lds + st * S::kStage + (h * S::HC + i) * 512 + wo);
+            wf[h][i] = *reinterpret_cast<const Codes*>(lds + wb * S::kW + (h * S::HC + i) * 1024 + (b ? wo1 : wo0));
     };
-    const auto read_scales = [&](int kb, int to) {
-        const uint8_t* base = lds + S::kScale + (kb & 1) * (S::kWS + S::kXS);
+    const auto read_sw = [&](int kp, int h) {
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(lds + S::kScale + (kp & 1) * (S::kWS + S::kXS)) +
+                            (wc * 16 + m) * 2 * S::HP + h * S::HP;
 #pragma unroll
-        for (int i = 0; i < S::NCP / 4; ++i) sw[to][i] = *reinterpret_cast<const uint32_t*>(base + swo + 4 * i);
-        if constexpr (F8) sx[to] = *reinterpret_cast<const uint32_t*>(base + sxo) - (q >> 1) * 0x05050505u;
+        for (int i = 0; i < S::HC; ++i) sw[h][i] = s[i] >> s_shift;
+    };
+    const auto read_sx = [&](int kp, int to) {
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(lds + S::kScale + (kp & 1) * (S::kWS + S::kXS) + S::kWS) +
+                            (wt * 16 + m) * NT;
+        if constexpr (F8)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sx[to][t] = (s[t] - (q >> 1) * 0x05050505u) >> s_shift;
     };
     f32x4 acc[NT][NC];
 #pragma unroll
@@ -525,48 +529,59 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
         for (int c = 0; c < NC; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     constexpr int kVm = 0x0f70, kLgkm0 = 0xc07f;   // wait for all but the low bits' vector loads; for all of LDS
-    issue_scales(0, 0);
-    issue(0, 0);
+    issue_scales(0);
+    issue_w(0, 0);
+    issue_x(0, 0);
     __builtin_amdgcn_sched_barrier(0);
-    // scale bytes of block kb go through register kb % 2 with four stages; with
-    // three the next ones are loaded when these have been put down
-    if constexpr (STAGES == 4) issue_scales(1, 1);
-    issue(1, 1);
+    if constexpr (STAGES == 4) issue_w(1, 1);
+    issue_x(1, 1);
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(kVm | (S::XL + S::WL + (STAGES == 4 ? F8 ? 2 : 1 : 0)));
-    put_scales(0, 0);
-    __builtin_amdgcn_sched_barrier(0);
-    issue_scales(STAGES - 2, 0);
-    if constexpr (STAGES == 4) issue(2, 2);
+    if constexpr (STAGES == 4) issue_x(2, 2);
+    __builtin_amdgcn_s_waitcnt(kVm | (STAGES == 4 ? S::WL + 2 * S::XL : S::XL));
+    put_scales(0);
     __builtin_amdgcn_s_waitcnt(kLgkm0);
     asm volatile("s_barrier" ::: "memory");
 #pragma unroll
     for (int t = 0; t < NT; ++t) read_x(0, t, 0);
-    read_w(0, 0);
-    read_scales(0, 0);
+    read_w(0, 0, 0);
+    read_sw(0, 0);
+    read_sx(0, 0);
 
-    int st = 0;
-    // P is kb % 2 where registers are held twice (a constant once inlined), else 0
+    // A pair's scales and the weights WB - 1 pairs ahead are loaded in its first
+    // block, before that block's tokens; the next pair's scales are put down in
+    // its second one.
+    int st = 0, wb = 0;
+    // P is kb % 2 (a constant once inlined)
     const auto block = [&](int kb, const int P) __attribute__((always_inline)) {
-        const int N = S::kDouble ? 1 - P : 0;
-        const int nx = st + 1 == STAGES ? 0 : st + 1;
+        const int D = S::kDouble ? P : 0, N = S::kDouble ? 1 - P : 0;
+        const int nx = st + 1 == STAGES ? 0 : st + 1, nw = wb + 1 == S::WB ? 0 : wb + 1, kp = kb >> 1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (h == 1) {
-                __builtin_amdgcn_s_waitcnt(kVm | S::kInFlight);
-                put_scales(kb + 1, STAGES == 3 ? 0 : 1 - P);
+            if (h == 0) {
+                read_w(wb, P, 1);
+                if (P == 0) read_sw(kp, 1);
+            } else {
+                if constexpr (STAGES == 3) __builtin_amdgcn_s_waitcnt(kVm);
+                else if (P == 0) __builtin_amdgcn_s_waitcnt(kVm | S::XL);
+                else __builtin_amdgcn_s_waitcnt(kVm | (S::WL + S::XL));
+                if (P == 1) put_scales(kp + 1);
                 __builtin_amdgcn_s_waitcnt(kLgkm0);
                 asm volatile("s_barrier" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
-                read_w(nx, 0);
-                read_scales(kb + 1, 1 - P);
+                read_w(P ? nw : wb, 1 - P, 0);
+                if (P == 1) {
+                    read_sw(kp + 1, 0);
+                    read_sx(kp + 1, 1);
+                }
                 if constexpr (S::kDouble)
 #pragma unroll
                     for (int t = 0; t < NT; ++t) read_x(nx, t, N);
-                issue_scales(kb + STAGES - 1, STAGES == 3 ? 0 : 1 - P);
-                issue(kb + STAGES - 1, st == 0 ? STAGES - 1 : st - 1);
-            } else {
-                read_w(st, 1);
+                if (P == 0) {
+                    issue_scales(kp + 1);
+                    issue_w(kp + S::WB - 1, wb == 0 ? S::WB - 1 : wb - 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                issue_x(kb + STAGES - 1, st == 0 ? STAGES - 1 : st - 1);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -576,20 +591,20 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
                     const Codes w = wf[h][i];
                     if constexpr (F8) {
                         const i32x8 a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-                        const u32x4 hi = xf[P][t][0], lo = xf[P][t][1];
+                        const u32x4 hi = xf[D][t][0], lo = xf[D][t][1];
                         const i32x8 b = {(int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3],
                                          (int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3]};
-                        acc[t][c] = mfma_f8(c & 3, t & 3, a, b, acc[t][c], (int)sw[P][c / 4], (int)sx[P]);
+                        acc[t][c] = mfma_f8(P, a, b, acc[t][c], (int)sw[h][i], (int)sx[0][t]);
                     } else {
                         if (t == 0) {
-                            const float scale = __uint_as_float((sw[P][c / 4] >> (8 * (c & 3)) & 0xffu) << 23);
+                            const float scale = __uint_as_float((sw[h][i] >> (16 * P) & 0xffu) << 23);
                             we[i][0] = mx_expand(w[0], scale);
                             we[i][1] = mx_expand(w[1], scale);
                         }
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                we[i][j], __builtin_bit_cast(bf16x8, xf[P][t][j]), acc[t][c], 0, 0, 0);
+                                we[i][j], __builtin_bit_cast(bf16x8, xf[D][t][j]), acc[t][c], 0, 0, 0);
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -597,21 +612,18 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
                     if (h == 1) read_x(nx, t, 0);
             }
         }
-        if constexpr (!S::kDouble) {
+        if (P == 1) {
+            if constexpr (F8)
 #pragma unroll
-            for (int i = 0; i < S::NCP / 4; ++i) sw[0][i] = sw[1][i];
-            sx[0] = sx[1];
+                for (int t = 0; t < NT; ++t) sx[0][t] = sx[1][t];
+            wb = nw;
         }
         st = nx;
     };
-    if constexpr (S::kDouble) {
-        for (int kb = 0; kb < blocks; kb += 2) {
-            block(kb, 0);
-            if (kb + 1 == blocks) break;
-            block(kb + 1, 1);
-        }
-    } else {
-        for (int kb = 0; kb < blocks; ++kb) block(kb, 0);
+    for (int kb = 0; kb < blocks; kb += 2) {
+        block(kb, 0);
+        if (kb + 1 == blocks) break;
+        block(kb + 1, 1);
     }
     // the loads past the last block are done before their stages are used again
     __builtin_amdgcn_s_waitcnt(0x0070);                          // vmcnt(0) lgkmcnt(0)
@@ -720,8 +732,10 @@ hipError_t launch_tiles(const MxIn& p, const MxOut& o, const MxSplit& sp, int n_
         const int64_t tiles = ((p.n_tok + tt - 1) / tt) * ((n_end + cc - 1) / cc);
         return (tiles + 255) / 256 * tt * cc;
     };
-    const int64_t large = cost(256, 256), mid = cost(128, 192), small = cost(128, 128);
-    if (large <= mid && large <= small) return tile<T, F8, 4, 8, 4, 2, 3>(p, o, sp, n_end, stream);
+    [[maybe_unused]] const int64_t large = cost(256, 256);
+    const int64_t mid = cost(128, 192), small = cost(128, 128);
+    if constexpr (F8)   // with expanded weights its registers spill
+        if (large <= mid && large <= small) return tile<T, F8, 4, 8, 4, 2, 3>(p, o, sp, n_end, stream);
     if (mid <= small) return tile<T, F8, 2, 6, 4, 2, 4>(p, o, sp, n_end, stream);
     return tile<T, F8, 2, 4, 4, 2, 4>(p, o, sp, n_end, stream);
 }
@@ -736,8 +750,8 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 MxSplit split_of(int64_t n_tok, int32_t n_in, void* workspace, size_t* bytes) {
     MxSplit s;
-    s.row = (n_in + 63) / 64 * 128;
-    const size_t data = up256((size_t)n_tok * s.row), scales = up256((size_t)n_tok * (s.row / 64));
+    s.pairs = (n_in + 127) / 128;
+    const size_t data = (size_t)n_tok * s.pairs * 256, scales = up256((size_t)n_tok * s.pairs * 4);
     s.data = static_cast<uint8_t*>(workspace);
     s.scales = s.data + data;
     s.flags = s.scales + scales;
