@@ -133,157 +133,166 @@ struct MxSplit {
     int pairs;         // of blocks, the last padded with zeros
 };
 
-// The four codes' dwords of four lanes 16 apart, transposed: lane row q gets
-// dword q of lane rows 0..3 in w[0..3].
-__device__ __forceinline__ void transpose4(u32x4& w) {
-    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-    w = u32x4{c[0], c[1], d[0], d[1]};
-}
-
 // Few tokens, and the strip of gates that the tile kernel leaves.  One
-// workgroup of 8 waves per 16 NT tokens and 16 NC channels; each wave
-// multiplies the whole tile over its eighth of the input axis, operands
-// straight from memory, D steps of 128 in flight, and the eight partial tiles
-// are added in LDS.  Lane l = 16 q + m loads row m's group q of a step as 16
-// bytes (32 codes); transposed over q, MFMA j of the four (16x16x32) takes
-// group j, lane q its codes 8q .. 8q+7, so tokens are read 64 bytes at a time.
-// W is the A operand: a lane's four results are consecutive channels of one
-// token.  A row's last step may reach past it: its tokens read zeros there and
-// its scales are 0, so whatever the codes are adds nothing.  At least four
-// groups of 32 (the scale bytes of a step come as one word).
+// workgroup of 8 waves per R tokens and 16 NC channels; each wave multiplies
+// the whole tile over its eighth of the input axis, in steps of 128, and the
+// eight partial tiles are added in LDS.  Operands go through LDS of the wave's
+// own (no barrier), D steps ahead, by loads that store straight into it: they
+// read rows in whole pieces of 64 and 256 bytes from neighbouring lanes, where
+// loads in the matrix operands' layout would take every lane's 16 bytes from
+// another row, at a quarter of the rate.  Lane l = 16 q + m holds row m's group
+// q of a step; MFMA j of the four (16x16x32) takes values 8j .. 8j+7 of all
+// four groups, so one scale serves a lane's four.  W is the A operand: a lane's
+// four results are consecutive channels of one token.  With R = 4 the tokens'
+// lanes repeat, and what repeats is left out at the end.  A row's last step may
+// reach past it: its tokens read zeros there and its scales are 0, so whatever
+// the codes are adds nothing.  At least four groups of 32 (the scale bytes of a
+// step come as one word).
 constexpr int kSkinnyWaves = 8;
 constexpr int kSkinnyThreads = 64 * kSkinnyWaves;
 
-constexpr size_t skinny_lds(int nt, int nc) {
-    return (size_t)kSkinnyWaves * 16 * nt * (16 * nc + 4) * sizeof(float);
-}
+template <int R, int NC, int D>
+struct SkinnyShape {
+    static constexpr int NT = (R + 15) / 16, XL = R / 4, kW = NC * 1024, kStage = kW + R * 256;
+    static constexpr int LD = 16 * NC + 4;
+    static constexpr int kLoads = kSkinnyWaves * D * kStage, kSums = kSkinnyWaves * R * LD * 4;
+    static constexpr int kBytes = kLoads > kSums ? kLoads : kSums;
+    static constexpr int kAhead = (D - 1) * (1 + NC + XL);   // loads of the steps behind the present one
+    static_assert((R == 4 || R % 16 == 0) && NC <= 4 && D <= 2 && kAhead < 64, "the schedule");
+};
 
-template <typename T, int NT, int NC>
+template <typename T, int R, int NC, int D>
 __device__ __forceinline__ void skinny_tile(const MxIn& p, const MxOut& o, int64_t t0, int n0) {
-    constexpr int D = 2;
-    extern __shared__ __align__(16) float red[];   // [8 waves][16 NT tokens][16 NC + 4 channels]
+    using S = SkinnyShape<R, NC, D>;
+    constexpr int NT = S::NT;
+    extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int toks = (int)min((int64_t)(16 * NT), p.n_tok - t0), rows = min(16 * NC, p.n_out - n0);
+    const int toks = (int)min((int64_t)R, p.n_tok - t0), rows = min(16 * NC, p.n_out - n0);
     const int half = p.n_in / 2, groups = p.n_in / 32;
     const int steps = (groups + 3) / 4, per = (steps + kSkinnyWaves - 1) / kSkinnyWaves;
     const int s_begin = wave * per, s_end = min(steps, s_begin + per);
     const auto x_rs = buf_rsrc(p.x + t0 * p.ld_x, ((toks - 1) * p.ld_x + p.n_in) * 2);
     const auto w_rs = buf_rsrc(p.codes + (int64_t)n0 * half, (int64_t)rows * half);
-    const uint8_t* sc = p.scales + (int64_t)n0 * groups;
-    int wo[NC], xo[NT];
-    uint32_t so[NC];
+    // Slot s of a token's 16 holds chunk s ^ row % 16, of a weight row's four
+    // chunk s ^ (row / 4) % 4, so the 16 rows of a fragment read spread over all
+    // banks.
+    int wo[NC], xo[S::XL], xchunk[S::XL];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int r = c * 16 + m;
-        wo[c] = offset_if(r < rows, r * half + q * 16);
-        so[c] = (uint32_t)min(r, rows - 1) * (uint32_t)groups;
+        const int r = c * 16 + (lane >> 2);
+        wo[c] = offset_if(r < rows, r * half + ((lane & 3) ^ ((r >> 2) & 3)) * 16);
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int r = t * 16 + m;
-        xo[t] = offset_if(r < toks, (int)(r * p.ld_x + q * 8) * 2);
+    for (int i = 0; i < S::XL; ++i) {
+        const int r = i * 4 + q;
+        xchunk[i] = m ^ (r & 15);
+        xo[i] = offset_if(r < toks, (int)(r * p.ld_x) * 2 + xchunk[i] * 16);
     }
-    // The scale bytes of groups 4 st .. 4 st + 3, the first lowest.  The load may
-    // be unaligned; where the row ends inside the four it starts earlier, by
-    // past() bytes that are shifted out once it has arrived.
+    // The scale bytes of groups 4 st .. 4 st + 3 of row `lane`, the first lowest.
+    // The load may be unaligned; where the row ends inside the four it starts
+    // earlier, by past() bytes that are shifted out once it has arrived.
     const auto past = [&](int st) { return max(0, st * 4 + 4 - groups); };
-    u32x4 xs[D][NT][4], ws[D][NC];
-    uint32_t ss[D][NC];
-    // steps from s_end on are loaded (the last one again) but not multiplied
+    const uint8_t* sc = p.scales + (int64_t)n0 * groups;
+    const uint32_t so = (uint32_t)min(lane, rows - 1) * (uint32_t)groups;
+    uint8_t* mine = lds + wave * (D * S::kStage);
+    uint32_t ss[D];
     const auto fetch = [&](int st, int b) {
-        st = min(st, steps - 1);
-        const uint8_t* s = sc + (st * 4 - past(st));
+        uint8_t* base = mine + b * S::kStage;
+        __builtin_memcpy(&ss[b], sc + (st * 4 - past(st)) + so, 4);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            ws[b][c] = __builtin_amdgcn_raw_buffer_load_b128(w_rs, wo[c], st * 64, 0);
-            __builtin_memcpy(&ss[b][c], s + so[c], 4);
-        }
+        for (int c = 0; c < NC; ++c) load_lds16(w_rs, base + c * 1024, wo[c], st * 64);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                xs[b][t][j] = __builtin_amdgcn_raw_buffer_load_b128(
-                    x_rs, offset_if(st * 4 + j < groups, xo[t]), min(st * 4 + j, groups - 1) * 64, 0);
+        for (int i = 0; i < S::XL; ++i)
+            load_lds16(x_rs, base + S::kW + i * 1024, offset_if(st * 128 + xchunk[i] * 8 < p.n_in, xo[i]), st * 256);
+        __builtin_amdgcn_sched_barrier(0);
     };
     f32x4 acc[NT][NC];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const auto multiply = [&](int st, int b) {
-        const int shift = 8 * past(st);
+    const int mx = m & (R < 16 ? R - 1 : 15);
+    const int w_at = m * 64 + ((q ^ (m >> 2)) & 3) * 16, x_at = S::kW + mx * 256;
+    const auto step = [&](int st, int b) __attribute__((always_inline)) {
+        constexpr int kVm0 = 0x0f70, kVmAhead = 0x0f70 | (S::kAhead & 15) | (S::kAhead >> 4) << 14;
+        if (st + D - 1 < s_end) __builtin_amdgcn_s_waitcnt(kVmAhead);
+        else __builtin_amdgcn_s_waitcnt(kVm0);
+        __builtin_amdgcn_sched_barrier(0);
+        const uint8_t* base = mine + b * S::kStage;
+        const uint32_t s = ss[b] >> (8 * past(st));
+        u32x4 w[NC], x[NT][4];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) w[c] = *reinterpret_cast<const u32x4*>(base + c * 1024 + w_at);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[t][j] = *reinterpret_cast<const u32x4*>(base + t * 4096 + x_at + ((q * 4 + j) ^ mx) * 16);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            transpose4(ws[b][c]);
-            const uint32_t s = ss[b][c] >> shift;
+            const uint32_t sr = (uint32_t)__builtin_amdgcn_ds_bpermute((c * 16 + m) * 4, (int)s);
+            const float scale = __uint_as_float((sr >> (8 * q) & 0xffu) << 23);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bf16x8 wf = mx_expand(ws[b][c][j], __uint_as_float((s >> (8 * j) & 0xffu) << 23));
+                const bf16x8 wf = mx_expand(w[c][j], scale);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     acc[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        wf, __builtin_bit_cast(bf16x8, xs[b][t][j]), acc[t][c], 0, 0, 0);
+                        wf, __builtin_bit_cast(bf16x8, x[t][j]), acc[t][c], 0, 0, 0);
             }
         }
+        __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the stage is read
+        __builtin_amdgcn_sched_barrier(0);
+        if (st + D < s_end) fetch(st + D, b);
     };
 #pragma unroll
-    for (int i = 0; i < D; ++i) fetch(s_begin + i, i);
-    __builtin_amdgcn_sched_barrier(0);
-    int st = s_begin;
-#pragma unroll 1
-    for (; st + D < s_end; st += D) {
-#pragma unroll
-        for (int i = 0; i < D; ++i) {
-            multiply(st + i, i);
-            fetch(st + D + i, i);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-#pragma unroll
     for (int i = 0; i < D; ++i)
-        if (st + i < s_end) multiply(st + i, i);
-    constexpr int LD = 16 * NC + 4;
-    float* mine = red + wave * (16 * NT * LD);
+        if (s_begin + i < s_end) fetch(s_begin + i, i);
+#pragma unroll 1
+    for (int st = s_begin; st < s_end; st += D) {
+        step(st, 0);
+        if constexpr (D == 2)
+            if (st + 1 < s_end) step(st + 1, 1);
+    }
+    __syncthreads();   // every wave is done with its stages
+    float* red = reinterpret_cast<float*>(lds);   // [8 waves][R tokens][16 NC + 4 channels]
+    if (R >= 16 || m < R)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            *reinterpret_cast<f32x4*>(&mine[(t * 16 + m) * LD + c * 16 + 4 * q]) = acc[t][c];
+            for (int c = 0; c < NC; ++c)
+                *reinterpret_cast<f32x4*>(&red[(wave * R + t * 16 + m) * S::LD + c * 16 + 4 * q]) = acc[t][c];
     __syncthreads();
 #pragma unroll 1
-    for (int i = threadIdx.x; i < 16 * NT * 4 * NC; i += kSkinnyThreads) {
+    for (int i = threadIdx.x; i < R * 4 * NC; i += kSkinnyThreads) {
         const int t = i / (4 * NC), c = (i % (4 * NC)) * 4;
         if (t >= toks || n0 + c >= p.n_out) continue;
         f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kSkinnyWaves; ++w)
-            y += *reinterpret_cast<const f32x4*>(&red[w * (16 * NT * LD) + t * LD + c]);
+            y += *reinterpret_cast<const f32x4*>(&red[(w * R + t) * S::LD + c]);
         mx_put4<T>(o, t0 + t, n0 + c, y);
     }
 }
 
-constexpr int skinny_waves_per_simd(int nt, int nc) { return nt * 16 + nc * 5 > 40 ? 2 : 4; }
-
-template <typename T, int NT, int NC>
-__global__ __launch_bounds__(kSkinnyThreads, skinny_waves_per_simd(NT, NC)) void mx_skinny_kernel(MxIn p, MxOut o,
-                                                                                                  int cols) {
-    skinny_tile<T, NT, NC>(p, o, (int64_t)(blockIdx.x / cols) * (16 * NT), (int)(blockIdx.x % cols) * (16 * NC));
+template <typename T, int R, int NC, int D>
+__global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, MxOut o, int cols) {
+    skinny_tile<T, R, NC, D>(p, o, (int64_t)(blockIdx.x / cols) * R, (int)(blockIdx.x % cols) * (16 * NC));
 }
 
 // The split of the tokens, one wave per token, 16 values per lane and round;
 // and in the first gate_wgs workgroups of the same launch the gates, which keep
 // fp32's accuracy: the skinny product over the strip of channels from c0 on.
-constexpr int kGateTokens = 1, kGateChannels = 4;   // in 16s
+constexpr int kGateTokens = 16, kGateChannels = 4;   // channels in 16s
+using GateShape = SkinnyShape<kGateTokens, kGateChannels, 1>;
 
 __global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxOut o, int c0, int cols,
                                                                      unsigned gate_wgs, MxSplit sp) {
     if (blockIdx.x < gate_wgs) {
-        skinny_tile<uint16_t, kGateTokens, kGateChannels>(p, o, (int64_t)(blockIdx.x / cols) * (16 * kGateTokens),
-                                                          c0 + (int)(blockIdx.x % cols) * (16 * kGateChannels));
+        skinny_tile<uint16_t, kGateTokens, kGateChannels, 1>(p, o, (int64_t)(blockIdx.x / cols) * kGateTokens,
+                                                             c0 + (int)(blockIdx.x % cols) * (16 * kGateChannels));
         return;
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, values = sp.pairs * 128;
@@ -686,27 +695,32 @@ bool fits(const void* p, int64_t ld, int elem, int vec) {
     return reinterpret_cast<uintptr_t>(p) % (vec * elem) == 0 && ld % vec == 0;
 }
 
-template <typename T, int NT, int NC>
+template <typename T, int R, int NC, int D = 2>
 hipError_t skinny(const MxIn& p, const MxOut& o, hipStream_t stream) {
-    constexpr size_t lds = skinny_lds(NT, NC);
+    constexpr int lds = SkinnyShape<R, NC, D>::kBytes;
+    static_assert(lds <= 160 * 1024, "fits");
     if (lds > 65536) {
         static std::atomic<uint64_t> done{0};
-        const hipError_t e = allow_dynamic_lds(&mx_skinny_kernel<T, NT, NC>, lds, &done);
+        const hipError_t e = allow_dynamic_lds(&mx_skinny_kernel<T, R, NC, D>, lds, &done);
         if (e != hipSuccess) return e;
     }
     const int cols = (p.n_out + 16 * NC - 1) / (16 * NC);
-    const dim3 grid((unsigned)(cols * ((p.n_tok + 16 * NT - 1) / (16 * NT))));
-    hipLaunchKernelGGL((mx_skinny_kernel<T, NT, NC>), grid, dim3(kSkinnyThreads), lds, stream, p, o, cols);
+    const dim3 grid((unsigned)(cols * ((p.n_tok + R - 1) / R)));
+    hipLaunchKernelGGL((mx_skinny_kernel<T, R, NC, D>), grid, dim3(kSkinnyThreads), lds, stream, p, o, cols);
     return hipGetLastError();
 }
 
 // The tokens' split and the channels from c0 on.
 hipError_t split(const MxIn& p, const MxOut& o, int c0, const MxSplit& sp, hipStream_t stream) {
-    constexpr size_t lds = skinny_lds(kGateTokens, kGateChannels);
-    static_assert(lds <= 65536, "the default limit");
+    constexpr int lds = GateShape::kBytes;
     const int cols = (p.n_out - c0 + 16 * kGateChannels - 1) / (16 * kGateChannels);
-    const int64_t gates = cols * ((p.n_tok + 16 * kGateTokens - 1) / (16 * kGateTokens));
+    const int64_t gates = cols * ((p.n_tok + kGateTokens - 1) / kGateTokens);
     const int64_t tokens = std::min<int64_t>((p.n_tok + kSkinnyWaves - 1) / kSkinnyWaves, 1 << 20);
+    if (gates && lds > 65536) {
+        static std::atomic<uint64_t> done{0};
+        const hipError_t e = allow_dynamic_lds(&mx_split_kernel, lds, &done);
+        if (e != hipSuccess) return e;
+    }
     hipLaunchKernelGGL(mx_split_kernel, dim3((unsigned)(gates + tokens)), dim3(kSkinnyThreads), gates ? lds : 0,
                        stream, p, o, c0, cols, (unsigned)gates, sp);
     return hipGetLastError();
@@ -724,14 +738,16 @@ hipError_t tile(const MxIn& p, const MxOut& o, const MxSplit& sp, int n_end, hip
     return hipGetLastError();
 }
 
+int64_t tiles_of(int64_t n_tok, int64_t n_out, int tt, int cc) {
+    return ((n_tok + tt - 1) / tt) * ((n_out + cc - 1) / cc);
+}
+int64_t rounds_of(int64_t tiles) { return (tiles + 255) / 256; }
+
 // The tile shape whose rounds of workgroups take the least: the measure is the
 // tile's area times the rounds.
 template <typename T, bool F8>
 hipError_t launch_tiles(const MxIn& p, const MxOut& o, const MxSplit& sp, int n_end, hipStream_t stream) {
-    const auto cost = [&](int tt, int cc) {
-        const int64_t tiles = ((p.n_tok + tt - 1) / tt) * ((n_end + cc - 1) / cc);
-        return (tiles + 255) / 256 * tt * cc;
-    };
+    const auto cost = [&](int tt, int cc) { return rounds_of(tiles_of(p.n_tok, n_end, tt, cc)) * tt * cc; };
     [[maybe_unused]] const int64_t large = cost(256, 256);
     const int64_t mid = cost(128, 192), small = cost(128, 128);
     if constexpr (F8)   // with expanded weights its registers spill
@@ -740,10 +756,21 @@ hipError_t launch_tiles(const MxIn& p, const MxOut& o, const MxSplit& sp, int n_
     return tile<T, F8, 2, 4, 4, 2, 4>(p, o, sp, n_end, stream);
 }
 
-constexpr int64_t kSkinnyTokens = 64;   // up to here the skinny kernel takes all channels
+// The skinny kernel takes the call, or the tile kernel.  A round of 256 skinny
+// workgroups of 32 tokens by 64 channels takes about 4 us and 1 more per 1024
+// inputs, a round of tiles 7 us and 1 per 107 (2048 -> 12352: 96 tokens 19.9
+// against 24.3 us, 128 tokens 25.5 against 24.2; 4096 -> 2048: 256 tokens 10.0
+// against 39.8 us).
+bool use_skinny(int64_t n_tok, int32_t n_in, int64_t n_out) {
+    if (n_in < 128) return false;
+    const int64_t few = rounds_of(tiles_of(n_tok, n_out, 32, 64)) * (4096 + n_in);
+    const int64_t many = std::min(rounds_of(tiles_of(n_tok, n_out, 128, 192)) * 192,
+                                  rounds_of(tiles_of(n_tok, n_out, 256, 256)) * 512) * (7 * 1024 + n_in * 19 / 2) / 192;
+    return n_tok <= 16 || few <= many;
+}
 
-bool use_split(int64_t n_tok, int32_t n_in, gdn_dtype out) {
-    return out == GDN_BF16 && n_tok > kSkinnyTokens && n_in >= 512;
+bool use_split(int64_t n_tok, int32_t n_in, int64_t n_out, gdn_dtype out) {
+    return out == GDN_BF16 && n_in >= 512 && !use_skinny(n_tok, n_in, n_out);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -763,33 +790,31 @@ template <typename T>
 hipError_t launch_few(const MxIn& p, const MxOut& o, hipStream_t stream) {
     // Bytes that the busiest CU takes in, the tile's tokens and weights: the
     // measure that separates the shapes where the axis is not the limit.
-    const auto cost = [&](int nt, int nc) {
-        const int64_t wgs = ((p.n_tok + 16 * nt - 1) / (16 * nt)) * ((p.n_out + 16 * nc - 1) / (16 * nc));
-        const int64_t toks = std::min<int64_t>(p.n_tok, 16 * nt);
-        return std::max<int64_t>(wgs, 256) * (toks * 4 + 16 * nc);
+    const auto cost = [&](int r, int nc) {
+        const int64_t wgs = ((p.n_tok + r - 1) / r) * ((p.n_out + 16 * nc - 1) / (16 * nc));
+        return (wgs + 255) / 256 * (std::min<int64_t>(p.n_tok, r) * 4 + 16 * nc);
     };
+    if (p.n_tok <= 4) return cost(4, 1) <= cost(4, 2) ? skinny<T, 4, 1>(p, o, stream) : skinny<T, 4, 2>(p, o, stream);
     int best = 0;
     int64_t least = INT64_MAX;
-    constexpr int shapes[][2] = {{1, 1}, {1, 2}, {1, 4}, {2, 2}, {2, 4}, {4, 4}};
-    for (int i = 0; i < 6; ++i) {
+    constexpr int shapes[][2] = {{16, 1}, {16, 2}, {16, 4}, {32, 4}};
+    for (int i = 0; i < 4; ++i) {
         const int64_t c = cost(shapes[i][0], shapes[i][1]);
         if (c < least) { least = c; best = i; }
     }
     switch (best) {
-        case 0: return skinny<T, 1, 1>(p, o, stream);
-        case 1: return skinny<T, 1, 2>(p, o, stream);
-        case 2: return skinny<T, 1, 4>(p, o, stream);
-        case 3: return skinny<T, 2, 2>(p, o, stream);
-        case 4: return skinny<T, 2, 4>(p, o, stream);
-        default: return skinny<T, 4, 4>(p, o, stream);
+        case 0: return skinny<T, 16, 1>(p, o, stream);
+        case 1: return skinny<T, 16, 2>(p, o, stream);
+        case 2: return skinny<T, 16, 4>(p, o, stream);
+        default: return skinny<T, 32, 4, 1>(p, o, stream);
     }
 }
 
 template <typename T>
 hipError_t launch_typed(const MxIn& p, const MxOut& o, void* workspace, hipStream_t stream) {
-    if (p.n_tok <= kSkinnyTokens && p.n_in >= 128) return launch_few<T>(p, o, stream);
+    if (use_skinny(p.n_tok, p.n_in, p.n_out)) return launch_few<T>(p, o, stream);
     if constexpr (sizeof(T) == 2) {
-        if (use_split(p.n_tok, p.n_in, GDN_BF16)) {
+        if (use_split(p.n_tok, p.n_in, p.n_out, GDN_BF16)) {
             size_t bytes;
             const MxSplit sp = split_of(p.n_tok, p.n_in, workspace, &bytes);
             const int n_end = o.end[3];
@@ -814,7 +839,7 @@ bool mx_proj_fits(int64_t n_tok, int64_t n_out) {
 size_t mx_proj_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out) {
     size_t bytes = 0;
     // whichever type the results have
-    if (use_split(n_tok, n_in, GDN_BF16)) split_of(n_tok, n_in, nullptr, &bytes);
+    if (use_split(n_tok, n_in, n_out, GDN_BF16)) split_of(n_tok, n_in, nullptr, &bytes);
     return bytes;
 }
 

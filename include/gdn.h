@@ -410,7 +410,7 @@ gdn_status gdn_mx_dequantize(int64_t rows, int32_t cols, const void* codes, cons
  *   x          device bf16 [n_tok][n_in], 16-byte aligned, ld_x elements
  *              between rows (a multiple of 8, at least n_in)
  *   y          device y_dtype [n_tok][n_out], ld_y elements between rows
- *   workspace  device, >= gdn_mx_proj_workspace_bytes (0 up to 64 tokens: NULL
+ *   workspace  device, >= gdn_mx_proj_workspace_bytes (0 for few tokens: NULL
  *              will do then), 256-byte aligned; scratch only
  * A single row's strides are not read.  Any n_out and n_tok; n_in a multiple
  * of GDN_MX_GROUP up to GDN_MX_MAX_IN, ld_x up to twice that, and fewer than
