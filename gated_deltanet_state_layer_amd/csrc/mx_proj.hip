@@ -285,7 +285,7 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
 // The split of the tokens, one wave per token, 16 values per lane and round;
 // and in the first gate_wgs workgroups of the same launch the gates, which keep
 // fp32's accuracy: the skinny product over the strip of channels from c0 on.
-constexpr int kGateTokens = 16, kGateChannels = 4;   // channels in 16s
+constexpr int kGateTokens = 16, kGateChannels = 2;   // channels in 16s
 using GateShape = SkinnyShape<kGateTokens, kGateChannels, 1>;
 
 __global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxOut o, int c0, int cols,
@@ -385,7 +385,7 @@ struct TileShape {
     static constexpr int kWS = WC * 16 * 2 * HP * 4, kXS = WT * 16 * NT * 4;
     static constexpr int kScale = kWeights + WB * kW, kBytes = kScale + 2 * (kWS + kXS);
     static constexpr bool kDouble = NT <= 2;
-    static_assert(TH == 512 && TT <= 256 && CC <= 256 && TT % (8 * WAVES) == 0, "a scale word per thread; whole loads");
+    static_assert(WAVES == 8 && TT <= 256 && CC <= 256 && TT % 64 == 0, "a scale word per thread; whole loads");
     static_assert(NC % 2 == 0 && (STAGES == 3 || STAGES == 4) && XL + WL < 16, "the schedule");
     // the epilogue's rows (fp32, 16 bytes apart) in the stages
     static constexpr int kRow = 16 * NC * 4 + 16;
@@ -464,15 +464,17 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
             load_lds16(w_rs, lds + S::kWeights + wb * S::kW + (wave * S::WL + i) * 1024, gw[i],
                        min(k, pairs - 1) * 64);
     };
-    // Scale words: the first half of the threads carries a weight row's each, the
-    // other a token's.  A weight row's word may be unaligned; where the row ends
+    // Scale words: the first four waves carry a weight row's per thread, the
+    // others a token's.  A weight row's word may be unaligned; where the row ends
     // inside it, it starts earlier, by past() bytes that are shifted out.
     const bool of_x = wave >= 4;
-    const int srow = tid & 255;
+    const int srow = tid & 255, rr = srow >> 4;
+    const auto past = [&](int kp) { return of_x ? 0 : max(0, kp * 4 + 4 - groups); };
     const uint8_t* s_at = of_x ? sp.scales + (t0 + min(srow, toks - 1)) * 4
                                : p.scales + (int64_t)(n0 + min(srow, rows - 1)) * groups;
     const int64_t s_step = of_x ? p.n_tok * 4 : 4;
-    const auto past = [&](int kp) { return of_x ? 0 : max(0, kp * 4 + 4 - groups); };
+    const int s_to = of_x ? S::kWS + ((rr / NT * 16 + (srow & 15)) * NT + rr % NT) * 4
+                          : ((rr / NC * 16 + (srow & 15)) * 2 * S::HP + rr % NC / S::HC * S::HP + rr % NC % S::HC) * 4;
     uint32_t s_in = 0;
     const auto issue_scales = [&](int k) {
         const int kp = min(k, pairs - 1);
@@ -487,9 +489,6 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
         }
         __builtin_amdgcn_sched_barrier(0);   // before the pair's other loads: the waits count on it
     };
-    const int rr = srow >> 4;
-    const int s_to = of_x ? S::kWS + ((rr / NT * 16 + (srow & 15)) * NT + rr % NT) * 4
-                          : ((rr / NC * 16 + (srow & 15)) * 2 * S::HP + rr % NC / S::HC * S::HP + rr % NC % S::HC) * 4;
     const auto put_scales = [&](int kp) {
         if (srow < (of_x ? F8 ? S::TT : 0 : S::CC))
             *reinterpret_cast<uint32_t*>(lds + S::kScale + (kp & 1) * (S::kWS + S::kXS) + s_to) =
@@ -757,15 +756,16 @@ hipError_t launch_tiles(const MxIn& p, const MxOut& o, const MxSplit& sp, int n_
 }
 
 // The skinny kernel takes the call, or the tile kernel.  A round of 256 skinny
-// workgroups of 32 tokens by 64 channels takes about 4 us and 1 more per 1024
-// inputs, a round of tiles 7 us and 1 per 107 (2048 -> 12352: 96 tokens 19.9
-// against 24.3 us, 128 tokens 25.5 against 24.2; 4096 -> 2048: 256 tokens 10.0
-// against 39.8 us).
+// workgroups of 32 tokens by 64 channels takes about 2 us and 1.8 more per 1024
+// inputs, a round of 128x192 tiles 5 us and 1 per 115, one of 256x256 tiles 8/3
+// of that (2048 -> 12352: 96 tokens 19.9 against 24.3 us, 128 tokens 25.5
+// against 24.2; 4096 -> 2048: 256 tokens 10.0 against 39.8 us, 1500 tokens 48.9
+// against 43.1).
 bool use_skinny(int64_t n_tok, int32_t n_in, int64_t n_out) {
     if (n_in < 128) return false;
-    const int64_t few = rounds_of(tiles_of(n_tok, n_out, 32, 64)) * (4096 + n_in);
-    const int64_t many = std::min(rounds_of(tiles_of(n_tok, n_out, 128, 192)) * 192,
-                                  rounds_of(tiles_of(n_tok, n_out, 256, 256)) * 512) * (7 * 1024 + n_in * 19 / 2) / 192;
+    const int64_t few = rounds_of(tiles_of(n_tok, n_out, 32, 64)) * (2048 + (int64_t)n_in * 9 / 5);
+    const int64_t many = std::min(rounds_of(tiles_of(n_tok, n_out, 128, 192)) * 3,
+                                  rounds_of(tiles_of(n_tok, n_out, 256, 256)) * 8) * (5 * 1024 + (int64_t)n_in * 89 / 10) / 3;
     return n_tok <= 16 || few <= many;
 }
 
