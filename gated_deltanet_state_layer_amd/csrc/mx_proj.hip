@@ -278,8 +278,8 @@ __device__ __forceinline__ void skinny_tile(const MxIn& p, const MxOut& o, int64
 }
 
 template <typename T, int R, int NC, int D>
-__global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, MxOut o, int cols) {
-    skinny_tile<T, R, NC, D>(p, o, (int64_t)(blockIdx.x / cols) * R, (int)(blockIdx.x % cols) * (16 * NC));
+__global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, MxOut o, int c0, int cols) {
+    skinny_tile<T, R, NC, D>(p, o, (int64_t)(blockIdx.x / cols) * R, c0 + (int)(blockIdx.x % cols) * (16 * NC));
 }
 
 // The split of the tokens, one wave per token, 16 values per lane and round;
@@ -422,9 +422,18 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wt = wave / WC, wc = wave % WC;
-    // consecutive tiles share their channels
-    const int64_t t0 = (int64_t)(blockIdx.x % tiles_t) * S::TT;
-    const int n0 = (int)(blockIdx.x / tiles_t) * S::CC;
+    // Consecutive tiles share their channels.  Workgroups go to the eight XCDs
+    // in turn: with fewer than eight tiles along the tokens each XCD takes a run
+    // of tiles, so that it reads the run's weights into its own cache once
+    // (500 x 2048 -> 12288 with gates 32.9 -> 31.9 us); with more, every eighth
+    // shares its tokens (8192 tokens 331 us, in runs 362).
+    unsigned idx = blockIdx.x;
+    if (tiles_t < 8) {
+        const unsigned xcd = idx % 8, per = gridDim.x / 8, rest = gridDim.x % 8;
+        idx = xcd * per + min(xcd, rest) + idx / 8;
+    }
+    const int64_t t0 = (int64_t)(idx % tiles_t) * S::TT;
+    const int n0 = (int)(idx / tiles_t) * S::CC;
     const int toks = (int)min((int64_t)S::TT, p.n_tok - t0), rows = min(S::CC, n_end - n0);
     const int half = p.n_in / 2, groups = p.n_in / 32, blocks = (groups + 1) / 2, pairs = (groups + 3) / 4;
     const auto x_rs = buf_rsrc(F8 ? nullptr : p.x + t0 * p.ld_x, ((toks - 1) * p.ld_x + p.n_in) * 2);
@@ -649,6 +658,19 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             *reinterpret_cast<f32x4*>(eb + m * S::kRow + (c * 16 + 4 * q) * 4) = acc[t][c];
+        if (!o.vec16) {   // element by element, neighbours in neighbouring lanes
+#pragma unroll 1
+            for (int i = lane; i < 16 * 16 * NC; i += 64) {
+                const int r = i / (16 * NC), c = i % (16 * NC);
+                const int64_t tok = tw + t * 16 + r;
+                if (tok >= p.n_tok || nw + c >= n_end) continue;
+                float y = reinterpret_cast<const float*>(eb + r * S::kRow)[c];
+                if constexpr (F8)
+                    if (y != y && sp.flags[tok] == 1) y = mx_dot(p, tok, nw + c);
+                mx_put<T>(o, tok, nw + c, y);
+            }
+            continue;
+        }
 #pragma unroll 1
         for (int i = lane; i < 16 * PIECES; i += 64) {
             const int r = i / PIECES, piece = (i % PIECES) * V;
@@ -658,7 +680,7 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
             if (tok >= p.n_tok || n >= n_end) continue;
             const f32x4 y0 = *reinterpret_cast<const f32x4*>(src);
             const f32x4 y1 = *reinterpret_cast<const f32x4*>(src + V - 4);
-            bool whole = o.vec16 && n + V <= end;
+            const bool whole = n + V <= end;
             // A token with an infinity (and no NaN) has no split: its results
             // are infinite or NaN, as the definition has them.
             bool again = false;
@@ -694,8 +716,9 @@ bool fits(const void* p, int64_t ld, int elem, int vec) {
     return reinterpret_cast<uintptr_t>(p) % (vec * elem) == 0 && ld % vec == 0;
 }
 
+// The channels from c0 on.
 template <typename T, int R, int NC, int D = 2>
-hipError_t skinny(const MxIn& p, const MxOut& o, hipStream_t stream) {
+hipError_t skinny(const MxIn& p, const MxOut& o, hipStream_t stream, int c0 = 0) {
     constexpr int lds = SkinnyShape<R, NC, D>::kBytes;
     static_assert(lds <= 160 * 1024, "fits");
     if (lds > 65536) {
@@ -703,9 +726,9 @@ hipError_t skinny(const MxIn& p, const MxOut& o, hipStream_t stream) {
         const hipError_t e = allow_dynamic_lds(&mx_skinny_kernel<T, R, NC, D>, lds, &done);
         if (e != hipSuccess) return e;
     }
-    const int cols = (p.n_out + 16 * NC - 1) / (16 * NC);
+    const int cols = (p.n_out - c0 + 16 * NC - 1) / (16 * NC);
     const dim3 grid((unsigned)(cols * ((p.n_tok + R - 1) / R)));
-    hipLaunchKernelGGL((mx_skinny_kernel<T, R, NC, D>), grid, dim3(kSkinnyThreads), lds, stream, p, o, cols);
+    hipLaunchKernelGGL((mx_skinny_kernel<T, R, NC, D>), grid, dim3(kSkinnyThreads), lds, stream, p, o, c0, cols);
     return hipGetLastError();
 }
 
@@ -742,31 +765,64 @@ int64_t tiles_of(int64_t n_tok, int64_t n_out, int tt, int cc) {
 }
 int64_t rounds_of(int64_t tiles) { return (tiles + 255) / 256; }
 
-// The tile shape whose rounds of workgroups take the least: the measure is the
-// tile's area times the rounds.
-template <typename T, bool F8>
-hipError_t launch_tiles(const MxIn& p, const MxOut& o, const MxSplit& sp, int n_end, hipStream_t stream) {
-    const auto cost = [&](int tt, int cc) { return rounds_of(tiles_of(p.n_tok, n_end, tt, cc)) * tt * cc; };
-    [[maybe_unused]] const int64_t large = cost(256, 256);
-    const int64_t mid = cost(128, 192), small = cost(128, 128);
-    if constexpr (F8)   // with expanded weights its registers spill
-        if (large <= mid && large <= small) return tile<T, F8, 4, 8, 4, 2, 3>(p, o, sp, n_end, stream);
-    if (mid <= small) return tile<T, F8, 2, 6, 4, 2, 4>(p, o, sp, n_end, stream);
-    return tile<T, F8, 2, 4, 4, 2, 4>(p, o, sp, n_end, stream);
+// Times in 1/1024 us, from which a call's kernels are picked.  A round of 256
+// skinny workgroups of 32 tokens by 64 channels takes about 2 us and 1.8 more
+// per 1024 inputs; of tiles about 5 us and, per 1024 inputs, 8 (128x128), 11.5
+// (128x192) or 23 (256x256).
+int64_t skinny_time(int64_t n_tok, int32_t n_in, int64_t n_out) {
+    return rounds_of(tiles_of(n_tok, n_out, 32, 64)) * (2048 + (int64_t)n_in * 9 / 5);
 }
 
-// The skinny kernel takes the call, or the tile kernel.  A round of 256 skinny
-// workgroups of 32 tokens by 64 channels takes about 2 us and 1.8 more per 1024
-// inputs, a round of 128x192 tiles 5 us and 1 per 115, one of 256x256 tiles 8/3
-// of that (2048 -> 12352: 96 tokens 19.9 against 24.3 us, 128 tokens 25.5
-// against 24.2; 4096 -> 2048: 256 tokens 10.0 against 39.8 us, 1500 tokens 48.9
-// against 43.1).
+// Tiles of one shape for the channels below n_main.  Where the last column of
+// tiles would cost a round for few channels, these are a skinny call of their
+// own (4096 x 2048 -> 12352: 12288 channels in 3 rounds, not 49 columns in 4).
+struct TilePlan {
+    int shape, n_main;
+    int64_t time;
+};
+constexpr int kTiles[3][3] = {{256, 256, 23 * 1024}, {128, 192, 11 * 1024 + 512}, {128, 128, 8 * 1024}};
+
+TilePlan plan_tiles(int64_t n_tok, int32_t n_in, int64_t n_out, bool large) {
+    TilePlan best{0, (int)n_out, INT64_MAX};
+    for (int i = large ? 0 : 1; i < 3; ++i) {
+        const int tt = kTiles[i][0], cc = kTiles[i][1];
+        const int64_t round = 5 * 1024 + (int64_t)n_in * kTiles[i][2] / 1024;
+        const int64_t whole = n_out / cc * cc;
+        const int64_t all = rounds_of(tiles_of(n_tok, n_out, tt, cc)) * round;
+        if (all < best.time) best = {i, (int)n_out, all};
+        if (whole == 0 || whole == n_out || n_in < 128) continue;
+        const int64_t strip = rounds_of(tiles_of(n_tok, whole, tt, cc)) * round + 2048 +
+                              skinny_time(n_tok, n_in, n_out - whole);
+        if (strip < best.time) best = {i, (int)whole, strip};
+    }
+    return best;
+}
+
+// Tiles for the channels below n_end; with expanded weights (no split) the
+// largest shape's registers spill.
+template <typename T, bool F8>
+hipError_t launch_tiles(const MxIn& p, const MxOut& o, const MxSplit& sp, int n_end, hipStream_t stream) {
+    const TilePlan plan = plan_tiles(p.n_tok, p.n_in, n_end, F8);
+    if (plan.n_main < n_end) {
+        MxIn rest = p;
+        rest.n_out = n_end;
+        const hipError_t e = skinny<T, 32, 4, 1>(rest, o, stream, plan.n_main);
+        if (e != hipSuccess) return e;
+    }
+    if constexpr (F8)
+        if (plan.shape == 0) return tile<T, F8, 4, 8, 4, 2, 3>(p, o, sp, plan.n_main, stream);
+    if (plan.shape == 1) return tile<T, F8, 2, 6, 4, 2, 4>(p, o, sp, plan.n_main, stream);
+    return tile<T, F8, 2, 4, 4, 2, 4>(p, o, sp, plan.n_main, stream);
+}
+
+// The skinny kernel takes the call, or the tile kernel (2048 -> 12352: 96 tokens
+// 19.9 against 24.3 us, 128 tokens 25.5 against 24.2; 4096 -> 2048: 256 tokens
+// 10.0 against 39.8 us, 1500 tokens 48.9 against 43.1).
 bool use_skinny(int64_t n_tok, int32_t n_in, int64_t n_out) {
     if (n_in < 128) return false;
-    const int64_t few = rounds_of(tiles_of(n_tok, n_out, 32, 64)) * (2048 + (int64_t)n_in * 9 / 5);
-    const int64_t many = std::min(rounds_of(tiles_of(n_tok, n_out, 128, 192)) * 3,
-                                  rounds_of(tiles_of(n_tok, n_out, 256, 256)) * 8) * (5 * 1024 + (int64_t)n_in * 89 / 10) / 3;
-    return n_tok <= 16 || few <= many;
+    // the split takes about 3 us, and its reads and writes
+    return n_tok <= 16 || skinny_time(n_tok, n_in, n_out) <=
+                              plan_tiles(n_tok, n_in, n_out, true).time + 3072 + n_tok * n_in / 1660;
 }
 
 bool use_split(int64_t n_tok, int32_t n_in, int64_t n_out, gdn_dtype out) {
