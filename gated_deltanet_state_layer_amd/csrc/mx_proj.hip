@@ -389,8 +389,8 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxO
 // A wave keeps its tokens' fragments of a block in registers and takes its
 // channels in two halves, all of a half times one token fragment after the
 // other; the next half's codes arrive meanwhile.  The block's one barrier
-// stands between the halves.  It says that the next block has arrived and the
-// previous one's stage is free, to be filled with the block STAGES - 1 ahead.
+// stands between the halves.  It says that the next block has arrived and this
+// one's stage is read out, to be filled with the block STAGES ahead.
 // Behind it the next block's token fragments are read, each as soon as the
 // second half is through with its predecessor, or where registers allow
 // (kDouble) all of them into a second set.
@@ -406,7 +406,7 @@ struct TileShape {
     static constexpr int kScale = kWeights + WB * kW, kBytes = kScale + 2 * (kWS + kXS);
     static constexpr bool kDouble = NT <= 2;
     static_assert(WAVES == 8 && TT <= 256 && CC <= 256 && TT % 64 == 0, "a scale word per thread; whole loads");
-    static_assert(NC % 2 == 0 && (STAGES == 3 || STAGES == 4) && XL + WL < 16, "the schedule");
+    static_assert(NC % 2 == 0 && (STAGES == 3 || STAGES == 4) && WL + (STAGES - 1) * XL < 16, "the schedule");
     // the epilogue's rows (fp32, 16 bytes apart) in the stages
     static constexpr int kRow = 16 * NC * 4 + 16;
     static_assert(WAVES * 16 * kRow <= kScale && kBytes <= 160 * 1024, "fits");
@@ -566,15 +566,19 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
         for (int c = 0; c < NC; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     constexpr int kVm = 0x0f70, kLgkm0 = 0xc07f;   // wait for all but the low bits' vector loads; for all of LDS
+    // the order in which the waits count: what follows a block's tokens
     issue_scales(0);
     issue_w(0, 0);
+    if constexpr (STAGES == 4) issue_w(1, 1);
     issue_x(0, 0);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (STAGES == 4) issue_w(1, 1);
     issue_x(1, 1);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (STAGES == 4) issue_x(2, 2);
-    __builtin_amdgcn_s_waitcnt(kVm | (STAGES == 4 ? S::WL + 2 * S::XL : S::XL));
+    issue_w(S::WB - 1, S::WB - 1);
+    issue_x(2, 2);
+    if constexpr (STAGES == 4) issue_x(3, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(kVm | (S::WL + (STAGES - 1) * S::XL));
     put_scales(0);
     __builtin_amdgcn_s_waitcnt(kLgkm0);
     asm volatile("s_barrier" ::: "memory");
@@ -584,9 +588,9 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
     read_sw(0, 0);
     read_sx(0, 0);
 
-    // A pair's scales and the weights WB - 1 pairs ahead are loaded in its first
-    // block, before that block's tokens; the next pair's scales are put down in
-    // its second one.
+    // The next pair's scales are loaded in a pair's first block, before that
+    // block's tokens, and put down in its second one, where the weights WB pairs
+    // ahead are loaded.
     int st = 0, wb = 0;
     // P is kb % 2 (a constant once inlined)
     const auto block = [&](int kb, const int P) __attribute__((always_inline)) {
@@ -598,9 +602,8 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
                 read_w(wb, P, 1);
                 if (P == 0) read_sw(kp, 1);
             } else {
-                if constexpr (STAGES == 3) __builtin_amdgcn_s_waitcnt(kVm);
-                else if (P == 0) __builtin_amdgcn_s_waitcnt(kVm | S::XL);
-                else __builtin_amdgcn_s_waitcnt(kVm | (S::WL + S::XL));
+                if (P == 0) __builtin_amdgcn_s_waitcnt(kVm | (S::WL + (STAGES - 2) * S::XL));
+                else __builtin_amdgcn_s_waitcnt(kVm | S::XL);
                 if (P == 1) put_scales(kp + 1);
                 __builtin_amdgcn_s_waitcnt(kLgkm0);
                 asm volatile("s_barrier" ::: "memory");
@@ -613,12 +616,10 @@ __global__ __launch_bounds__(64 * WT * WC, 2) void mx_tile_kernel(MxIn p, MxOut 
                 if constexpr (S::kDouble)
 #pragma unroll
                     for (int t = 0; t < NT; ++t) read_x(nx, t, N);
-                if (P == 0) {
-                    issue_scales(kp + 1);
-                    issue_w(kp + S::WB - 1, wb == 0 ? S::WB - 1 : wb - 1);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                issue_x(kb + STAGES - 1, st == 0 ? STAGES - 1 : st - 1);
+                if (P == 0) issue_scales(kp + 1);
+                else issue_w(kp + S::WB, wb);
+                __builtin_amdgcn_sched_barrier(0);
+                issue_x(kb + STAGES, st);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
