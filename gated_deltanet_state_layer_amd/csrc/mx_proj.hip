@@ -6,7 +6,7 @@
 // way is to expand codes in registers and multiply in bf16.  For bf16 results of
 // many tokens the tokens are split into two 8-bit floats instead, and codes go
 // into the scaled matrix instructions as they are: as many matrix cycles, none
-// for expanding (8192 x 2048 -> 12288 with gates 330-340 us against 487; a
+// for expanding (8192 x 2048 -> 12288 with gates 320-345 us against 487; a
 // library product of that size on bf16 weights takes 358).  The 8-bit
 // instructions' sums are less exact than the bf16 ones': of 2048 -> 4096, 4 bf16
 // results in 1000 differ from the float64 sum's rounding, 4 in 100000 the plain
@@ -374,10 +374,11 @@ __global__ __launch_bounds__(kSkinnyThreads, 4) void mx_split_kernel(MxIn p, MxO
 // codes as they are, through STAGES - 1.  The four scale bytes of a pair go
 // through a register to a two-stage area ordered so that a lane reads those of
 // its rows side by side.  What bounds the kernel is this feed, not the matrix
-// units (8192 x 2048 -> 12288: 309 us; 255 without the loads, 259 without the
-// products), so each load takes as much of a row at once as LDS holds.  Four
-// waves of twice the area read LDS less but hide less: 360 for 321 us, and 500
-// tokens 38.2 for 34.0.
+// units, so each load takes as much of a row at once as LDS holds: 8192 x 2048
+// -> 12288 took 309 us, 255 without the loads, 259 without the products, before
+// loads went one block further ahead (300 us; the matrix units are then busy
+// 57 % of the time, at 2.0 GHz).  Four waves of twice the area read LDS less but
+// hide less: 360 for 321 us with the split, and 500 tokens 38.2 for 34.0.
 //
 // bf16 (F8 false): lane q of MFMA j (16x16x32) takes k = 16 q + 8 j ..: one
 // 8-byte read of codes serves both MFMAs, expanded in registers.
