@@ -51,6 +51,10 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
     reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// fp32 elements at any address: 16-byte accesses need only four-byte alignment.
+__device__ __forceinline__ void load8_any(const float* p, float* x) { __builtin_memcpy(x, p, 32); }
+__device__ __forceinline__ void store8_any(float* p, const float* x) { __builtin_memcpy(p, x, 32); }
+
 constexpr int kNormThreads = 256;
 // A launch holds fewer than 2^32 threads; larger calls loop.
 constexpr int64_t kMaxGrid = 1 << 20;
@@ -64,15 +68,19 @@ struct BlockNorm {
     float res_scale, w_offset, inv_hidden, eps;
 };
 
+// How a row is read and written: in aligned 16-byte accesses; in unaligned ones
+// with a ragged last vector (fp32 operands of odd widths and strides); element
+// by element (bf16 ones, whose rows may start between dwords).
+enum class Rows { kAligned, kUnaligned, kElements };
+
 // One workgroup of TPR threads per row.  Element j of vector i of thread t is
-// column (i * TPR + t) * 8 + j with VEC (16-byte accesses), and column
-// (8 i + j) * TPR + t without (odd widths and strides: neighbouring threads
-// read neighbouring elements).
-template <typename TIO, typename TR, int TPR, int NV, bool VEC>
+// column (i * TPR + t) * 8 + j, and column (8 i + j) * TPR + t by elements
+// (neighbouring threads read neighbouring elements).
+template <typename TIO, typename TR, int TPR, int NV, Rows ROWS>
 __global__ __launch_bounds__(TPR) void block_norm_kernel(BlockNorm p) {
     __shared__ float red[2][TPR / 64];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const auto col = [&](int i, int j) { return VEC ? (i * TPR + t) * 8 + j : (8 * i + j) * TPR + t; };
+    const auto col = [&](int i, int j) { return ROWS != Rows::kElements ? (i * TPR + t) * 8 + j : (8 * i + j) * TPR + t; };
     const auto row_sum = [&](float s, int slot) {
         s = wave_sum(s);
         if constexpr (TPR > 64) {
@@ -85,21 +93,25 @@ __global__ __launch_bounds__(TPR) void block_norm_kernel(BlockNorm p) {
         return s;
     };
     const auto read = [&](const auto* src, float* v, int i) {
-        if constexpr (VEC) {
+        if constexpr (ROWS == Rows::kAligned) {
             if (col(i, 0) < p.hidden) load8(src + col(i, 0), v);
             else
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = 0.f;
         } else {
+            if constexpr (ROWS == Rows::kUnaligned)
+                if (col(i, 7) < p.hidden) return load8_any(src + col(i, 0), v);
             using T = std::remove_cv_t<std::remove_pointer_t<decltype(src)>>;
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = col(i, j) < p.hidden ? Io<T>::load(src, col(i, j)) : 0.f;
         }
     };
     const auto write = [&](auto* dst, const float* v, int i) {
-        if constexpr (VEC) {
+        if constexpr (ROWS == Rows::kAligned) {
             if (col(i, 0) < p.hidden) store8(dst + col(i, 0), v);
         } else {
+            if constexpr (ROWS == Rows::kUnaligned)
+                if (col(i, 7) < p.hidden) return store8_any(dst + col(i, 0), v);
             using T = std::remove_pointer_t<decltype(dst)>;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -158,16 +170,31 @@ __global__ __launch_bounds__(TPR) void block_norm_kernel(BlockNorm p) {
     }
 }
 
-template <typename TIO, typename TR, bool VEC>
-void launch_block_norm_typed(const BlockNorm& p, hipStream_t stream) {
+template <typename TIO, typename TR, Rows ROWS>
+void launch_block_norm_rows(const BlockNorm& p, hipStream_t stream) {
     const dim3 grid((unsigned)std::min<int64_t>(p.n_tok, kMaxGrid));
     const int vecs = (p.hidden + 7) / 8;
-    if (vecs <= kNormThreads)
-        hipLaunchKernelGGL((block_norm_kernel<TIO, TR, 256, 1, VEC>), grid, dim3(256), 0, stream, p);
-    else if (vecs <= 4 * kNormThreads)
-        hipLaunchKernelGGL((block_norm_kernel<TIO, TR, 256, 4, VEC>), grid, dim3(256), 0, stream, p);
+    // A vector a thread as long as a workgroup reaches: 256 threads with four each
+    // took 134.7 us for 3000 x 5003 (bf16, fp32 residual, element by element) and
+    // 64 x 4096 3.7 us, 1024 with one 78.2 and 3.1.
+    if (vecs <= 256)
+        hipLaunchKernelGGL((block_norm_kernel<TIO, TR, 256, 1, ROWS>), grid, dim3(256), 0, stream, p);
+    else if (vecs <= 512)
+        hipLaunchKernelGGL((block_norm_kernel<TIO, TR, 512, 1, ROWS>), grid, dim3(512), 0, stream, p);
+    else if (vecs <= 1024)
+        hipLaunchKernelGGL((block_norm_kernel<TIO, TR, 1024, 1, ROWS>), grid, dim3(1024), 0, stream, p);
     else
-        hipLaunchKernelGGL((block_norm_kernel<TIO, TR, 1024, 2, VEC>), grid, dim3(1024), 0, stream, p);
+        hipLaunchKernelGGL((block_norm_kernel<TIO, TR, 1024, 2, ROWS>), grid, dim3(1024), 0, stream, p);
+}
+
+template <typename TIO, typename TR>
+void launch_block_norm_typed(const BlockNorm& p, bool aligned, hipStream_t stream) {
+    if (aligned) return launch_block_norm_rows<TIO, TR, Rows::kAligned>(p, stream);
+    // unaligned vectors pay above 2048 elements (fp32: 1237 x 1999 9.5 us by
+    // elements, 10.1 so; 3000 x 5003 62.7 and 53.2)
+    if constexpr (sizeof(TIO) == 4 && sizeof(TR) == 4)
+        if (p.hidden > 2048) return launch_block_norm_rows<TIO, TR, Rows::kUnaligned>(p, stream);
+    launch_block_norm_rows<TIO, TR, Rows::kElements>(p, stream);
 }
 
 struct GatedNorm {
@@ -235,18 +262,10 @@ hipError_t launch_block_norm(int64_t n_tok, int32_t hidden, gdn_dtype io_dtype, 
     const bool vec = hidden % 8 == 0 && ok(y, ld_y) && ok(r, ld_r) && ok(r_out, ld_ro) && ok(x, ld_x) &&
                      ok(w_post, 0) && ok(w_pre, 0);
     const bool io16 = io_dtype == GDN_BF16, r16 = res_dtype == GDN_BF16;
-    if (io16 && r16)
-        vec ? launch_block_norm_typed<uint16_t, uint16_t, true>(p, stream)
-            : launch_block_norm_typed<uint16_t, uint16_t, false>(p, stream);
-    else if (io16)
-        vec ? launch_block_norm_typed<uint16_t, float, true>(p, stream)
-            : launch_block_norm_typed<uint16_t, float, false>(p, stream);
-    else if (r16)
-        vec ? launch_block_norm_typed<float, uint16_t, true>(p, stream)
-            : launch_block_norm_typed<float, uint16_t, false>(p, stream);
-    else
-        vec ? launch_block_norm_typed<float, float, true>(p, stream)
-            : launch_block_norm_typed<float, float, false>(p, stream);
+    if (io16 && r16) launch_block_norm_typed<uint16_t, uint16_t>(p, vec, stream);
+    else if (io16) launch_block_norm_typed<uint16_t, float>(p, vec, stream);
+    else if (r16) launch_block_norm_typed<float, uint16_t>(p, vec, stream);
+    else launch_block_norm_typed<float, float>(p, vec, stream);
     return hipGetLastError();
 }
 
