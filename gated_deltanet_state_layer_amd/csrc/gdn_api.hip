@@ -620,8 +620,8 @@ static int64_t mx_in_proj_channels(const gdn_pool* pool, bool with_z) {
     return (int64_t)P.c_conv + (with_z ? (int64_t)P.h_v * P.d : 0) + 2 * (int64_t)P.h_v;
 }
 
-static gdn_status mx_workspace_ok(size_t need, const void* workspace, size_t workspace_bytes) {
-    if (workspace_bytes < need || (need > 0 && !workspace)) return GDN_ERR_WORKSPACE;
+// No size needs scratch memory; one that is given has to be aligned all the same.
+static gdn_status mx_workspace_ok(const void* workspace) {
     return workspace && !aligned(workspace, kAlign) ? GDN_ERR_INVALID_ARG : GDN_OK;
 }
 
@@ -629,13 +629,13 @@ gdn_status gdn_mx_proj_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_ou
     const gdn_status st = mx_proj_args(n_tok, n_in, n_out);
     if (st != GDN_OK) return st;
     if (!bytes) return GDN_ERR_INVALID_ARG;
-    *bytes = mx_proj_workspace_bytes(n_tok, n_in, n_out);
+    *bytes = 0;
     return GDN_OK;
 }
 
 gdn_status gdn_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
                        const void* codes, const uint8_t* scales, gdn_dtype y_dtype, void* y, int64_t ld_y,
-                       void* workspace, size_t workspace_bytes, void* stream) {
+                       void* workspace, size_t /*workspace_bytes*/, void* stream) {
     gdn_status st = mx_proj_args(n_tok, n_in, n_out);
     if (st != GDN_OK) return st;
     if (!dtype_ok(y_dtype)) return GDN_ERR_INVALID_ARG;
@@ -648,10 +648,10 @@ gdn_status gdn_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x
     }
     if (ld_x < n_in || ld_x % 8 != 0 || ld_y < n_out) return GDN_ERR_INVALID_ARG;
     if (ld_x > 2 * GDN_MX_MAX_IN) return GDN_ERR_UNSUPPORTED;
-    st = mx_workspace_ok(mx_proj_workspace_bytes(n_tok, n_in, n_out), workspace, workspace_bytes);
+    st = mx_workspace_ok(workspace);
     if (st != GDN_OK) return st;
-    return launch_mx_proj(n_tok, n_in, n_out, x, ld_x, codes, scales, y_dtype, y, ld_y, workspace,
-                          as_stream(stream)) == hipSuccess
+    return launch_mx_proj(n_tok, n_in, n_out, x, ld_x, codes, scales, y_dtype, y, ld_y, as_stream(stream)) ==
+                   hipSuccess
                ? GDN_OK
                : GDN_ERR_HIP;
 }
@@ -663,13 +663,13 @@ gdn_status gdn_mx_in_proj_workspace_bytes(const gdn_pool* pool, int64_t n_tok, i
     const gdn_status st = mx_proj_args(n_tok, hidden, n_out);
     if (st != GDN_OK) return st;
     if (!bytes) return GDN_ERR_INVALID_ARG;
-    *bytes = mx_proj_workspace_bytes(n_tok, hidden, (int32_t)n_out);
+    *bytes = 0;
     return GDN_OK;
 }
 
 gdn_status gdn_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
                           const void* codes, const uint8_t* scales, void* q, void* k, void* v, void* z,
-                          float* a, float* b, void* workspace, size_t workspace_bytes, void* stream) {
+                          float* a, float* b, void* workspace, size_t /*workspace_bytes*/, void* stream) {
     if (!pool) return GDN_ERR_INVALID_ARG;
     const int64_t n_out = mx_in_proj_channels(pool, z != nullptr);
     gdn_status st = mx_proj_args(n_tok, hidden, n_out);
@@ -680,10 +680,10 @@ gdn_status gdn_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, c
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(q, io) || !aligned(k, io) || !aligned(v, io) ||
         !aligned(z, io) || !aligned(a, 4) || !aligned(b, 4))
         return GDN_ERR_INVALID_ARG;
-    st = mx_workspace_ok(mx_proj_workspace_bytes(n_tok, hidden, (int32_t)n_out), workspace, workspace_bytes);
+    st = mx_workspace_ok(workspace);
     if (st != GDN_OK) return st;
-    return launch_mx_in_proj(pool, n_tok, hidden, x, codes, scales, q, k, v, z, a, b, workspace,
-                             as_stream(stream)) == hipSuccess
+    return launch_mx_in_proj(pool, n_tok, hidden, x, codes, scales, q, k, v, z, a, b, as_stream(stream)) ==
+                   hipSuccess
                ? GDN_OK
                : GDN_ERR_HIP;
 }

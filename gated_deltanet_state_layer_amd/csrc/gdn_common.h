@@ -197,13 +197,12 @@ hipError_t launch_mx_quantize(int64_t rows, int32_t cols, gdn_dtype dtype, const
 hipError_t launch_mx_dequantize(int64_t rows, int32_t cols, gdn_dtype dtype, const void* codes,
                                 const uint8_t* scales, void* dst, hipStream_t stream);
 bool mx_proj_fits(int64_t n_tok, int64_t n_out);
-size_t mx_proj_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out);
 hipError_t launch_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
                           const void* codes, const uint8_t* scales, gdn_dtype y_dtype, void* y,
-                          int64_t ld_y, void* workspace, hipStream_t stream);
+                          int64_t ld_y, hipStream_t stream);
 hipError_t launch_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
                              const void* codes, const uint8_t* scales, void* q, void* k, void* v,
-                             void* z, float* a, float* b, void* workspace, hipStream_t stream);
+                             void* z, float* a, float* b, hipStream_t stream);
 size_t prefill_workspace_bytes(const gdn_pool* pool, int32_t n_seq, int64_t total_tokens,
                                int32_t chunk);
 // The static prefill scratch (kStaticScratchBytes on every device): its

@@ -406,16 +406,18 @@ gdn_status gdn_mx_dequantize(int64_t rows, int32_t cols, const void* codes, cons
                              gdn_dtype dtype, void* dst, void* stream);
 
 /* Projection with 4-bit weights: y = x W^T, W as above with n_out rows of n_in
- * weights; products are exact and accumulate in fp32.
+ * weights; products are exact and accumulate in fp32, and a bf16 result is that
+ * sum rounded once.  The order of the additions, and with it a result's last
+ * bit, may differ between calls of other sizes, not between calls of one size.
  *   x          device bf16 [n_tok][n_in], 16-byte aligned, ld_x elements
  *              between rows (a multiple of 8, at least n_in)
  *   y          device y_dtype [n_tok][n_out], ld_y elements between rows
- *   workspace  device, >= gdn_mx_proj_workspace_bytes (0 for few tokens: NULL
- *              will do then), 256-byte aligned; scratch only
+ *   workspace  device, >= gdn_mx_proj_workspace_bytes, 256-byte aligned; scratch
+ *              only.  That size is 0 for every call: NULL will do
  * A single row's strides are not read.  Any n_out and n_tok; n_in a multiple
  * of GDN_MX_GROUP up to GDN_MX_MAX_IN, ld_x up to twice that, and fewer than
  * 2^22 tiles of 64 tokens by 64 channels (UNSUPPORTED otherwise).  Weights of
- * 2^128 and more (scale bytes 253 and 254) may count as infinite. */
+ * 2^128 and more (scale bytes 253 and 254) count as infinite. */
 #define GDN_MX_MAX_IN 1048576
 gdn_status gdn_mx_proj_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out, size_t* bytes);
 gdn_status gdn_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
