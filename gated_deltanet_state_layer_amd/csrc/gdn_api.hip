@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "gdn_common.h"
+#include "mx_plan.h"
 
 namespace gdn {
 size_t decode_verify_lds_bytes(const gdn_pool* pool, int32_t n_tok);

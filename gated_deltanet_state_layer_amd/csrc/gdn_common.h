@@ -196,7 +196,6 @@ hipError_t launch_mx_quantize(int64_t rows, int32_t cols, gdn_dtype dtype, const
                               uint8_t* scales, hipStream_t stream);
 hipError_t launch_mx_dequantize(int64_t rows, int32_t cols, gdn_dtype dtype, const void* codes,
                                 const uint8_t* scales, void* dst, hipStream_t stream);
-bool mx_proj_fits(int64_t n_tok, int64_t n_out);
 hipError_t launch_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
                           const void* codes, const uint8_t* scales, gdn_dtype y_dtype, void* y,
                           int64_t ld_y, hipStream_t stream);

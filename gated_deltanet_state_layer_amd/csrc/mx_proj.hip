@@ -13,6 +13,7 @@
 
 #include "gdn_common.h"
 #include "mfma_split.h"
+#include "mx_plan.h"
 
 namespace gdn {
 namespace {
@@ -140,8 +141,7 @@ struct MxIn {
 // 5.0 TB/s would take 2.7, a launch takes 1.9), 64 tokens 4096 -> 2048 5.9 us;
 // operand-order loads 7.7 and 9.8.  D = 1 where two steps do not fit: 32 tokens
 // by 64 channels of LDS would be 192 KiB.
-constexpr int kSkinnyWaves = 8;
-constexpr int kSkinnyThreads = 64 * kSkinnyWaves;
+constexpr int kSkinnyThreads = kMxWorkgroup, kSkinnyWaves = kSkinnyThreads / 64;
 
 template <int R, int NC, int D>
 struct SkinnyShape {
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
 // stands between the halves.  It says that the next block has arrived and this
 // one's stage is read out, to be filled with the block four ahead.  Behind it
 // the next block's token fragments are read into a second set of registers.
-constexpr int kTileTokens = 128, kTileThreads = 512, kStages = 4, kWeightStages = 3;
+constexpr int kTileTokens = kMxTileTokens, kTileThreads = kMxWorkgroup, kStages = 4, kWeightStages = 3;
 
 template <int NC>
 struct TileShape {
@@ -552,9 +552,8 @@ bool fits(const void* p, int64_t ld, int elem, int vec) {
     return reinterpret_cast<uintptr_t>(p) % (vec * elem) == 0 && ld % vec == 0;
 }
 
-// The channels from c0 on.
 template <typename T, int R, int NC, int D = 2>
-hipError_t skinny(const MxIn& p, const MxOut& o, hipStream_t stream, int c0 = 0) {
+hipError_t skinny(const MxIn& p, const MxOut& o, const MxLaunch& l, hipStream_t stream) {
     constexpr int lds = SkinnyShape<R, NC, D>::kBytes;
     static_assert(lds <= 160 * 1024, "fits");
     if (lds > 65536) {
@@ -562,118 +561,48 @@ hipError_t skinny(const MxIn& p, const MxOut& o, hipStream_t stream, int c0 = 0)
         const hipError_t e = allow_dynamic_lds(&mx_skinny_kernel<T, R, NC, D>, lds, &done);
         if (e != hipSuccess) return e;
     }
-    const int cols = (p.n_out - c0 + 16 * NC - 1) / (16 * NC);
-    const dim3 grid((unsigned)(cols * ((p.n_tok + R - 1) / R)));
-    hipLaunchKernelGGL((mx_skinny_kernel<T, R, NC, D>), grid, dim3(kSkinnyThreads), lds, stream, p, o, c0, cols);
+    const int cols = (l.c1 - l.c0 + 16 * NC - 1) / (16 * NC);
+    hipLaunchKernelGGL((mx_skinny_kernel<T, R, NC, D>), dim3((unsigned)l.workgroups), dim3(kSkinnyThreads), lds, stream,
+                       p, o, l.c0, cols);
     return hipGetLastError();
 }
 
 template <typename T, int NC>
-hipError_t tile(const MxIn& p, const MxOut& o, int n_end, hipStream_t stream) {
+hipError_t tile(const MxIn& p, const MxOut& o, const MxLaunch& l, hipStream_t stream) {
     using S = TileShape<NC>;
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_dynamic_lds(&mx_tile_kernel<T, NC>, S::kBytes, &done);
     if (e != hipSuccess) return e;
-    const int tiles_t = (int)((p.n_tok + kTileTokens - 1) / kTileTokens), tiles_c = (n_end + S::CC - 1) / S::CC;
-    hipLaunchKernelGGL((mx_tile_kernel<T, NC>), dim3((unsigned)tiles_t * tiles_c), dim3(kTileThreads), S::kBytes, stream,
-                       p, o, tiles_t, n_end);
+    hipLaunchKernelGGL((mx_tile_kernel<T, NC>), dim3((unsigned)l.workgroups), dim3(kTileThreads), S::kBytes, stream, p,
+                       o, (int)((p.n_tok + kTileTokens - 1) / kTileTokens), l.c1);
     return hipGetLastError();
 }
 
-int64_t tiles_of(int64_t n_tok, int64_t n_out, int tt, int cc) {
-    return ((n_tok + tt - 1) / tt) * ((n_out + cc - 1) / cc);
-}
-int64_t rounds_of(int64_t tiles) { return (tiles + 255) / 256; }
-
-// Times in 1/1024 us, from which a call's kernels are picked.  A round of 256
-// skinny workgroups of 32 tokens by 64 channels takes about 2 us and 1.8 more
-// per 1024 inputs; of tiles about 5 us and, per 1024 inputs, 8 (128x128) or 11.5
-// (128x192).
-int64_t skinny_time(int64_t n_tok, int32_t n_in, int64_t n_out) {
-    return rounds_of(tiles_of(n_tok, n_out, 32, 64)) * (2048 + (int64_t)n_in * 9 / 5);
-}
-
-// Tiles of 128 tokens by `channels` for the channels below n_main.  Where the last column of
-// tiles would cost a round for few channels, these are a skinny call of their
-// own (4096 x 2048 -> 12352: 12288 channels in 3 rounds, not 49 columns in 4).
-struct TilePlan {
-    int channels, n_main;
-    int64_t time;
-};
-constexpr int kTiles[2][2] = {{192, 11 * 1024 + 512}, {128, 8 * 1024}};
-
-TilePlan plan_tiles(int64_t n_tok, int32_t n_in, int64_t n_out) {
-    TilePlan best{0, (int)n_out, INT64_MAX};
-    for (const auto& t : kTiles) {
-        const int cc = t[0];
-        const int64_t round = 5 * 1024 + (int64_t)n_in * t[1] / 1024;
-        const int64_t whole = n_out / cc * cc;
-        const int64_t all = rounds_of(tiles_of(n_tok, n_out, kTileTokens, cc)) * round;
-        if (all < best.time) best = {cc, (int)n_out, all};
-        if (whole == 0 || whole == n_out || n_in < 128) continue;
-        const int64_t strip = rounds_of(tiles_of(n_tok, whole, kTileTokens, cc)) * round + 2048 +
-                              skinny_time(n_tok, n_in, n_out - whole);
-        if (strip < best.time) best = {cc, (int)whole, strip};
-    }
-    return best;
-}
-
 template <typename T>
-hipError_t launch_tiles(const MxIn& p, const MxOut& o, hipStream_t stream) {
-    const TilePlan plan = plan_tiles(p.n_tok, p.n_in, p.n_out);
-    if (plan.n_main < p.n_out) {
-        const hipError_t e = skinny<T, 32, 4, 1>(p, o, stream, plan.n_main);
-        if (e != hipSuccess) return e;
-    }
-    return plan.channels == 192 ? tile<T, 6>(p, o, plan.n_main, stream) : tile<T, 4>(p, o, plan.n_main, stream);
-}
-
-// The skinny kernel takes the call, or the tile kernel (2048 -> 12352: 96 tokens
-// 19.9 against 24.3 us, 128 tokens 25.5 against 24.2; 4096 -> 2048: 256 tokens
-// 10.0 against 39.8 us, 1500 tokens 48.9 against 43.1).
-bool use_skinny(int64_t n_tok, int32_t n_in, int64_t n_out) {
-    if (n_in < 128) return false;
-    return n_tok <= 16 || skinny_time(n_tok, n_in, n_out) <= plan_tiles(n_tok, n_in, n_out).time;
-}
-
-template <typename T>
-hipError_t launch_few(const MxIn& p, const MxOut& o, hipStream_t stream) {
-    // Bytes that the busiest CU takes in, the tile's tokens and weights: the
-    // measure that separates the shapes where the axis is not the limit.
-    const auto cost = [&](int r, int nc) {
-        const int64_t wgs = ((p.n_tok + r - 1) / r) * ((p.n_out + 16 * nc - 1) / (16 * nc));
-        return (wgs + 255) / 256 * (std::min<int64_t>(p.n_tok, r) * 4 + 16 * nc);
-    };
-    if (p.n_tok <= 4) return cost(4, 1) <= cost(4, 2) ? skinny<T, 4, 1>(p, o, stream) : skinny<T, 4, 2>(p, o, stream);
-    int best = 0;
-    int64_t least = INT64_MAX;
-    constexpr int shapes[][2] = {{16, 1}, {16, 2}, {16, 4}, {32, 4}};
-    for (int i = 0; i < 4; ++i) {
-        const int64_t c = cost(shapes[i][0], shapes[i][1]);
-        if (c < least) { least = c; best = i; }
-    }
-    switch (best) {
-        case 0: return skinny<T, 16, 1>(p, o, stream);
-        case 1: return skinny<T, 16, 2>(p, o, stream);
-        case 2: return skinny<T, 16, 4>(p, o, stream);
-        default: return skinny<T, 32, 4, 1>(p, o, stream);
+hipError_t launch_one(const MxIn& p, const MxOut& o, const MxLaunch& l, hipStream_t stream) {
+    if (l.tile) return l.channels == 192 ? tile<T, 6>(p, o, l, stream) : tile<T, 4>(p, o, l, stream);
+    switch (l.tokens * 256 + l.channels) {
+        case 4 * 256 + 16: return skinny<T, 4, 1>(p, o, l, stream);
+        case 4 * 256 + 32: return skinny<T, 4, 2>(p, o, l, stream);
+        case 16 * 256 + 16: return skinny<T, 16, 1>(p, o, l, stream);
+        case 16 * 256 + 32: return skinny<T, 16, 2>(p, o, l, stream);
+        case 16 * 256 + 64: return skinny<T, 16, 4>(p, o, l, stream);
+        case 32 * 256 + 64: return skinny<T, 32, 4, 1>(p, o, l, stream);
+        default: return hipErrorInvalidValue;   // a shape without a kernel
     }
 }
 
 template <typename T>
 hipError_t launch_typed(const MxIn& p, const MxOut& o, hipStream_t stream) {
-    if (use_skinny(p.n_tok, p.n_in, p.n_out)) return launch_few<T>(p, o, stream);
-    return launch_tiles<T>(p, o, stream);
+    const MxPlan plan = mx_plan(p.n_tok, p.n_in, p.n_out);
+    for (int i = 0; i < plan.n; ++i) {
+        const hipError_t e = launch_one<T>(p, o, plan.launch[i], stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
-
-// Every launch stays below 2^32 threads: the most are 512 for each 32 tokens by
-// 64 channels.
-bool mx_proj_fits(int64_t n_tok, int64_t n_out) {
-    const int64_t t = n_tok / 64 + 1, c = n_out / 64 + 1;
-    return t < (1 << 22) && t * c < (1 << 22);
-}
 
 hipError_t launch_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
                           const void* codes, const uint8_t* scales, gdn_dtype y_dtype, void* y,
