@@ -38,27 +38,30 @@ inline bool mx_proj_fits(int64_t n_tok, int64_t n_out) {
 }
 
 // Times in 1/1024 us, from which a call's kernels are picked.  A round of 256
-// skinny workgroups of 32 tokens by 64 channels takes about 2 us and 1.8 more
-// per 1024 inputs; of tiles about 5 us and, per 1024 inputs, 8 (128x128) or 11.5
-// (128x192).
+// skinny workgroups of 32 tokens by 64 channels takes about 2.5 us and 1.6 more
+// per 1024 inputs; of tiles about 4 us and, per 1024 inputs, 8.8 (128x128) or
+// 12.2 (128x192).  Fitted to 19 token counts of 24 to 8192 for each of eleven
+// pairs of 128 to 8192 inputs and 1001 to 16384 channels: what is picked takes
+// 0.5 % longer than the fastest way on average, 17 % at worst.
 inline int64_t mx_skinny_time(int64_t n_tok, int32_t n_in, int64_t n_out) {
-    return mx_rounds(mx_tiles(n_tok, n_out, 32, 64)) * (2048 + (int64_t)n_in * 9 / 5);
+    return mx_rounds(mx_tiles(n_tok, n_out, 32, 64)) * (2560 + (int64_t)n_in * 8 / 5);
 }
 
 // Tiles of 128 tokens by `channels` for the channels below n_main.  Where the
 // last column of tiles would cost a round for few channels, these are a skinny
-// call of their own (4096 x 2048 -> 12352: 12288 channels in 3 rounds, not 49 columns in 4).
+// call of their own (500 x 2048 -> 12352: 64 columns in one round and a strip
+// 39.0 us, 65 columns in two 61.0).
 struct MxTiles {
     int channels, n_main;
     int64_t time;
 };
-constexpr int kMxTiles[2][2] = {{192, 11 * 1024 + 512}, {128, 8 * 1024}};
+constexpr int kMxTiles[2][2] = {{192, 12 * 1024 + 205}, {128, 8 * 1024 + 819}};
 
 inline MxTiles mx_plan_tiles(int64_t n_tok, int32_t n_in, int64_t n_out) {
     MxTiles best{0, (int)n_out, INT64_MAX};
     for (const auto& t : kMxTiles) {
         const int cc = t[0];
-        const int64_t round = 5 * 1024 + (int64_t)n_in * t[1] / 1024;
+        const int64_t round = 4 * 1024 + (int64_t)n_in * t[1] / 1024;
         const int64_t whole = n_out / cc * cc;
         const int64_t all = mx_rounds(mx_tiles(n_tok, n_out, kMxTileTokens, cc)) * round;
         if (all < best.time) best = {cc, (int)n_out, all};
@@ -89,8 +92,8 @@ inline MxLaunch mx_plan_skinny(int64_t n_tok, int64_t n_out) {
 }
 
 // The skinny kernel takes the call, or the tile kernel (2048 -> 12352: 96 tokens
-// 19.9 against 24.3 us, 128 tokens 25.5 against 24.2; 4096 -> 2048: 256 tokens
-// 10.0 against 39.8 us, 1500 tokens 48.9 against 43.1).
+// 20.4 against 23.6 us, 128 tokens 26.3 against 23.6; 4096 -> 2048: 1000 tokens
+// 34.7 against 42.3 us, 1536 tokens 51.1 against 42.6).
 inline MxPlan mx_plan(int64_t n_tok, int32_t n_in, int64_t n_out) {
     const MxTiles t = mx_plan_tiles(n_tok, n_in, n_out);
     if (n_in >= 128 && (n_tok <= 16 || mx_skinny_time(n_tok, n_in, n_out) <= t.time))
