@@ -53,3 +53,22 @@ def paths(n_tok, n_in, n_out):
     """The launches' kernels: "skinny", "tile128", "tile192", "strip" (the skinny
     kernel behind tiles)."""
     return [f"tile{p.channels}" if p.tile else "strip" if p.c0 else "skinny" for p in plan(n_tok, n_in, n_out)]
+
+
+# Sizes that reach the tile kernels, with the launches they take: both tiles,
+# with and without a strip behind them; inputs that end inside 64 and inside
+# 128, fewer than four groups of inputs; even and odd widths.
+TILE_CASES = [
+    (300, 96, 700, ["tile128"]), (129, 64, 4097, ["tile128"]), (700, 544, 1500, ["tile128"]),
+    (700, 2080, 3000, ["tile128"]), (300, 1056, 12301, ["tile192"]), (2600, 1184, 2050, ["tile192"]),
+    (700, 512, 8200, ["tile192", "strip"]), (500, 1184, 12353, ["tile192", "strip"]),
+]
+# In-projections: tokens, hidden, h_k, h_v, d; the gates are the last channels.
+TILE_IN_PROJ = [
+    (1100, 512, 4, 8, 128, ["tile128"]), (300, 544, 16, 32, 128, ["tile192"]),
+    (500, 544, 16, 32, 128, ["tile192", "strip"]),
+]
+
+
+def in_proj_channels(h_k, h_v, d):
+    return 2 * h_k * d + 2 * h_v * d + 2 * h_v

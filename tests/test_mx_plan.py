@@ -2,7 +2,7 @@
 the call, each channel once, and stay within what a launch may hold."""
 import pytest
 
-from mx_plan import fits, paths, plan
+from mx_plan import TILE_CASES, TILE_IN_PROJ, fits, in_proj_channels, paths, plan
 
 TOKENS = [1, 4, 5, 16, 17, 64, 129, 1000, 8192, 65537, (1 << 20) + 1, (1 << 24) + 3, 1 << 26, (1 << 27) - 1, 1 << 27,
           (1 << 27) + 1, 200_000_000, (1 << 28) - 65]
@@ -41,3 +41,14 @@ def test_launches_cover_the_call_within_the_grid(n_tok, n_in):
 ])
 def test_the_faster_kernels_are_taken(n_tok, n_in, n_out, want):
     assert paths(n_tok, n_in, n_out) == want
+
+
+@pytest.mark.parametrize("n_tok,n_in,n_out,want", TILE_CASES)
+def test_tile_cases_reach_the_tiles(n_tok, n_in, n_out, want):
+    """The sizes that the GPU tests of the tile kernels rely on."""
+    assert paths(n_tok, n_in, n_out) == want
+
+
+@pytest.mark.parametrize("n_tok,hidden,h_k,h_v,d,want", TILE_IN_PROJ)
+def test_tile_in_projections_reach_the_tiles(n_tok, hidden, h_k, h_v, d, want):
+    assert paths(n_tok, hidden, in_proj_channels(h_k, h_v, d)) == want
