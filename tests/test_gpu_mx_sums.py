@@ -121,3 +121,17 @@ def test_in_proj_sums_in_32_bits(G):
     want = torch.split(_exact(x, _decode(codes, scales), 2.0 ** -5), widths, 1)
     for name, y in zip("qkvz", want):
         assert _count(r[name].reshape(n_tok, -1), y.to(BF).double()) == 0, name
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("scale", [127, 187])
+@pytest.mark.parametrize("n_tok,n_in,n_out", SIZES)
+def test_subnormal_tokens(G, n_tok, n_in, n_out, scale, out):
+    """Tokens below the smallest normal bf16 value are multiplied as they are."""
+    gen = torch.Generator(device="cuda").manual_seed(n_tok + scale)
+    codes, scales = _weights(n_out, n_in, gen, scale, scale + 1)
+    m = torch.randint(-127, 128, (n_tok, n_in), generator=gen, device="cuda").double()
+    x = (m * 2.0 ** -133).to(BF)
+    assert torch.equal(x.double(), m * 2.0 ** -133)
+    want = _exact(m, _decode(codes, scales), 2.0 ** (scale - 128)) * 2.0 ** -133
+    assert _count(_call(G, x, codes, scales, out), want.to(out).double()) == 0
