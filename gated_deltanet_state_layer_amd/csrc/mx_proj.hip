@@ -314,11 +314,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wt = wave / S::WC, wc = wave % S::WC;
     // Consecutive tiles share their channels.  Workgroups go to the eight XCDs
-    // in turn: with fewer than eight tiles along the tokens each XCD takes a run
-    // of tiles, so that it reads the run's weights into its own cache once; with
-    // more, every eighth shares its tokens.
+    // in turn: with up to eight tiles along the tokens each XCD takes a run of
+    // tiles, so that it reads the run's weights into its own cache once (2048 ->
+    // 12352: 500 tokens 39.3 us in turn, 38.2 in runs, 1000 tokens 69.7 and 66.1);
+    // with more, every eighth shares its tokens (4096 -> 4096: 4096 tokens 155.0
+    // us in turn, 171.7 in runs; at 16 tiles either may win by 3 %).
     unsigned idx = blockIdx.x;
-    if (tiles_t < 8) {
+    if (tiles_t <= 8) {
         const unsigned xcd = idx % 8, per = gridDim.x / 8, rest = gridDim.x % 8;
         idx = xcd * per + min(xcd, rest) + idx / 8;
     }

@@ -174,7 +174,7 @@ void launch_block_norm_rows(const BlockNorm& p, hipStream_t stream) {
     const int vecs = (p.hidden + 7) / 8;
     // A vector a thread as far as a workgroup reaches, and no fewer than 256
     // threads: with 256 at every width 3000 x 5003 (bf16, fp32 residual, element by
-    // element) took 134.7 us, 78.6 so, and 64 x 4096 in fp32 3.7 us, 3.1 so.
+    // element) took 134.9 us, 78.5 so, and 64 x 4096 in fp32 3.6 us, 3.2 so.
     if (vecs <= 256)
         hipLaunchKernelGGL((block_norm_kernel<TIO, TR, 256, 1, ROWS>), grid, dim3(256), 0, stream, p);
     else if (vecs <= 512)
