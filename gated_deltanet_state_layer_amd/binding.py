@@ -31,6 +31,8 @@ GDN_STATIC_SCRATCH_BYTES = 64 << 20
 GDN_BLOCK_NORM_MAX_HIDDEN = 16384
 GDN_MX_GROUP = 32
 GDN_MX_MAX_IN = 1048576
+GDN_BEAM_MAX = 64
+GDN_LORA_MAX_RANK = 128
 
 EXPORTED = (
     "gdn_pool_bytes", "gdn_pool_create", "gdn_pool_destroy", "gdn_slot_reset",
@@ -40,7 +42,9 @@ EXPORTED = (
     "gdn_ring_commit", "gdn_ring_flush", "gdn_in_proj_workspace_bytes", "gdn_in_proj",
     "gdn_pool_error", "gdn_status_string", "gdn_block_norm", "gdn_gated_norm",
     "gdn_mx_quantize", "gdn_mx_dequantize", "gdn_mx_proj_workspace_bytes", "gdn_mx_proj",
-    "gdn_mx_in_proj_workspace_bytes", "gdn_mx_in_proj",
+    "gdn_mx_in_proj_workspace_bytes", "gdn_mx_in_proj", "gdn_mx_proj_lora_workspace_bytes",
+    "gdn_mx_proj_lora", "gdn_mx_in_proj_lora_workspace_bytes", "gdn_mx_in_proj_lora",
+    "gdn_batch_maps", "gdn_beam_select_workspace_bytes", "gdn_beam_select", "gdn_slot_reorder",
 )
 
 
@@ -104,6 +108,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "gdn_mx_proj": [I64, I32, I32, P, I64, P, P, I32, P, I64, P, SZ, P],
         "gdn_mx_in_proj_workspace_bytes": [P, I64, I32, I32, PSZ],
         "gdn_mx_in_proj": [P, I64, I32, P, P, P, P, P, P, P, P, P, P, SZ, P],
+        "gdn_mx_proj_lora_workspace_bytes": [I64, I32, I32, I32, PSZ],
+        "gdn_mx_proj_lora": [I64, I32, I32, P, I64, P, P, I32, I32, P, P, P, P, I32, P, I64, P, SZ, P],
+        "gdn_mx_in_proj_lora_workspace_bytes": [P, I64, I32, I32, I32, PSZ],
+        "gdn_mx_in_proj_lora": [P, I64, I32, P, P, P, I32, I32, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
+        "gdn_batch_maps": [P, I32, P, I64, P, P, P, P, P, P, I32, P, I32, P, I32, P, P, I32, P],
+        "gdn_beam_select_workspace_bytes": [I32, I32, I32, I32, PSZ],
+        "gdn_beam_select": [I32, I32, I32, I32, I32, P, I64, P, P, I32, P, P, P, P, P, SZ, P],
+        "gdn_slot_reorder": [P, I32, I32, P, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -334,6 +346,118 @@ def mx_proj(x, codes, scales, out, workspace=None, stream=None):
     return out
 
 
+def _on_current_device(*tensors):
+    """The library launches on the current device: operands live there."""
+    dev = _device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _workspace(ws):
+    """A workspace's pointer and bytes."""
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("workspace: not a contiguous device tensor")
+    return ws.data_ptr(), ws.nbytes
+
+
+def _lora_args(a, b, scale, token_adapter, n_tok, n_in, n_out):
+    """Checks the adapters' tensors; their count and rank."""
+    if a is None or a.dim() != 3 or a.shape[2] != n_in:
+        raise ValueError(f"lora_a: expected [adapters, rank, {n_in}]")
+    n, rank = a.shape[0], a.shape[1]
+    if n:
+        _need(a, "lora_a", n * rank * n_in, torch.bfloat16)
+        if b is None or b.shape != (n, n_out, rank):
+            raise ValueError(f"lora_b: expected [{n}, {n_out}, {rank}]")
+        _need(b, "lora_b", n * n_out * rank, torch.bfloat16)
+        _need(scale, "lora_scale", n, torch.float32)
+        _need(token_adapter, "token_adapter", n_tok, torch.int32)
+    return n, rank
+
+
+def mx_proj_lora_workspace_bytes(n_tok, n_in, n_out, rank):
+    lib = load_library()
+    n = ctypes.c_size_t()
+    _check(lib.gdn_mx_proj_lora_workspace_bytes(n_tok, n_in, n_out, rank, ctypes.byref(n)),
+           "gdn_mx_proj_lora_workspace_bytes")
+    return n.value
+
+
+def mx_proj_lora(x, codes, scales, lora_a, lora_b, lora_scale, token_adapter, out, workspace=None,
+                 stream=None):
+    """gdn_mx_proj_lora: mx_proj, and to each token's row lora_scale[i] (x A_i^T)
+    B_i^T of its adapter i = token_adapter[token] (-1: none).  lora_a [adapters,
+    rank, n_in] and lora_b [adapters, n_out, rank] are bfloat16."""
+    lib = _lib or load_library()
+    if x.dim() != 2 or out.dim() != 2:
+        raise ValueError("x and out: expected [tokens, channels]")
+    (n_tok, n_in), n_out = x.shape, out.shape[1]
+    ld_x = _rows(x, "x", (n_tok, n_in), torch.bfloat16)
+    ld_y = _rows(out, "out", (n_tok, n_out), out.dtype)
+    code = _dtype(out, "out")
+    _need(codes, "codes", n_out * n_in // 2, torch.uint8)
+    _need(scales, "scales", n_out * n_in // GDN_MX_GROUP, torch.uint8)
+    n, rank = _lora_args(lora_a, lora_b, lora_scale, token_adapter, n_tok, n_in, n_out)
+    _on_current_device(out, lora_a, token_adapter)
+    ws, ws_bytes = _workspace(workspace)
+    _check(lib.gdn_mx_proj_lora(n_tok, n_in, n_out, x.data_ptr(), ld_x, codes.data_ptr(),
+                                scales.data_ptr(), n, rank, _ptr(lora_a), _ptr(lora_b),
+                                _ptr(lora_scale), _ptr(token_adapter), code, out.data_ptr(), ld_y, ws,
+                                ws_bytes, _stream(stream)), "gdn_mx_proj_lora")
+    return out
+
+
+def beam_select_workspace_bytes(n_req, width, vocab, n_out):
+    lib = load_library()
+    n = ctypes.c_size_t()
+    _check(lib.gdn_beam_select_workspace_bytes(n_req, width, vocab, n_out, ctypes.byref(n)),
+           "gdn_beam_select_workspace_bytes")
+    return n.value
+
+
+def beam_select(logits, scores, parents, tokens, scores_out, finished=None, finished_out=None, eos=-1,
+                workspace=None, stream=None):
+    """gdn_beam_select: from logits [requests, width, vocab] (bfloat16 or
+    float32; rows may be strided, evenly) and the beams' scores [requests, width],
+    the best continuations: parents, tokens (int32) and scores_out (float32)
+    [requests, n_out]; finished and finished_out are uint8."""
+    lib = _lib or load_library()
+    if logits.dim() != 3 or scores_out.dim() != 2:
+        raise ValueError("logits: expected [requests, width, vocab], scores_out [requests, n_out]")
+    n_req, width, vocab = logits.shape
+    n_out = scores_out.shape[1]
+    code = _dtype(logits, "logits")
+    ld = vocab
+    if not logits.is_contiguous():
+        ld = logits.stride(1) if width > 1 else logits.stride(0)
+        if (vocab > 1 and logits.stride(2) != 1) or \
+                (n_req > 1 and width > 1 and logits.stride(0) != width * ld):
+            raise ValueError("logits: rows are not contiguous and evenly spaced")
+    if not logits.is_cuda:
+        raise ValueError("logits: not a device tensor")
+    for t, name, shape, dt in ((scores, "scores", (n_req, width), torch.float32),
+                               (parents, "parents", (n_req, n_out), torch.int32),
+                               (tokens, "tokens", (n_req, n_out), torch.int32),
+                               (scores_out, "scores_out", (n_req, n_out), torch.float32),
+                               (finished, "finished", (n_req, width), torch.uint8),
+                               (finished_out, "finished_out", (n_req, n_out), torch.uint8)):
+        if t is None and shape and name.startswith("finished"):
+            continue
+        if t is None or t.shape != shape:
+            raise ValueError(f"{name}: expected {shape}")
+        _need(t, name, t.numel(), dt)
+    _on_current_device(logits, scores, parents)
+    ws, ws_bytes = _workspace(workspace)
+    _check(lib.gdn_beam_select(n_req, width, vocab, n_out, code, logits.data_ptr(), ld,
+                               scores.data_ptr(), _ptr(finished), eos, parents.data_ptr(),
+                               tokens.data_ptr(), scores_out.data_ptr(), _ptr(finished_out), ws,
+                               ws_bytes, _stream(stream)), "gdn_beam_select")
+    return parents, tokens, scores_out
+
+
 class Pool:
     """A slot pool over torch-owned device buffers.
 
@@ -408,6 +532,63 @@ class Pool:
         _need(dst_ids, "dst_ids", src_ids.numel(), torch.int32)
         _check(lib.gdn_slot_copy(self._h, int(src_ids.numel()), _ptr(src_ids), _ptr(dst_ids),
                                  _stream(stream)), "gdn_slot_copy")
+
+    def reorder(self, slots, parents, slots_out, stream=None):
+        """gdn_slot_reorder: after beam selection, slot slots_out[r, i] holds
+        what slot slots[r, parents[r, i]] held; slots_out [requests, width] is a
+        permutation of slots and may be slots itself."""
+        lib = _lib or load_library()
+        if slots.dim() != 2 or slots.shape != parents.shape or slots.shape != slots_out.shape:
+            raise ValueError("slots, parents and slots_out: expected [requests, width]")
+        n_req, width = slots.shape
+        n = n_req * width
+        _need(slots, "slots", n, torch.int32)
+        _need(parents, "parents", n, torch.int32)
+        _need(slots_out, "slots_out", n, torch.int32)
+        _on_current_device(slots, parents, slots_out)
+        _check(lib.gdn_slot_reorder(self._h, n_req, width, slots.data_ptr(), parents.data_ptr(),
+                                    slots_out.data_ptr(), _stream(stream)), "gdn_slot_reorder")
+        return slots_out
+
+    def batch_maps(self, lens, cu_seqlens, max_tokens=None, last_rows=None, token_seq=None, past=None,
+                   token_pos=None, adapter_ids=None, n_adapters=0, token_adapter=None, ckpt_every=0,
+                   free_slots=None, ckpt_offsets=None, ckpt_slots=None, stream=None):
+        """gdn_batch_maps: from the lengths of a batch's requests, cu_seqlens
+        and whichever of the other maps is given (all int32).  The per-token maps
+        share one length, the tokens there is room for; without any, max_tokens
+        says it."""
+        lib = _lib or load_library()
+        n, room = lens.numel(), max_tokens
+        for t, name in ((token_seq, "token_seq"), (token_pos, "token_pos"),
+                        (token_adapter, "token_adapter")):
+            if t is not None:
+                if room is None:
+                    room = t.numel()
+                _need(t, name, room, torch.int32)
+                if t.numel() != room:
+                    raise ValueError(f"{name}: {t.numel()} elements, expected {room}")
+        if room is None:
+            room = 2 ** 31 - 2
+        if token_adapter is not None and adapter_ids is None:
+            raise ValueError("token_adapter needs adapter_ids")
+        _need(lens, "lens", n, torch.int32)
+        _need(cu_seqlens, "cu_seqlens", n + 1, torch.int32)
+        for t, name in ((last_rows, "last_rows"), (past, "past"), (adapter_ids, "adapter_ids")):
+            if t is not None:
+                _need(t, name, n, torch.int32)
+        n_free = max_ckpt = 0
+        if ckpt_every > 0:
+            _need(ckpt_offsets, "ckpt_offsets", n + 1, torch.int32)
+            n_free = 0 if free_slots is None else free_slots.numel()
+            max_ckpt = 0 if ckpt_slots is None else ckpt_slots.numel()
+            _need(free_slots, "free_slots", n_free, torch.int32)
+            _need(ckpt_slots, "ckpt_slots", max_ckpt, torch.int32)
+        _on_current_device(lens, cu_seqlens, token_seq)
+        _check(lib.gdn_batch_maps(self._h, n, _ptr(lens), room, cu_seqlens.data_ptr(), _ptr(last_rows),
+                                  _ptr(token_seq), _ptr(past), _ptr(token_pos), _ptr(adapter_ids),
+                                  n_adapters, _ptr(token_adapter), ckpt_every, _ptr(free_slots), n_free,
+                                  _ptr(ckpt_offsets), _ptr(ckpt_slots), max_ckpt, _stream(stream)),
+               "gdn_batch_maps")
 
     def decode(self, layer, slot_ids, q, k, v, a, b, conv_w, out, stream=None):
         lib = load_library()
@@ -590,6 +771,44 @@ class Pool:
         _check(lib.gdn_mx_in_proj(self._h, n_tok, hidden, _ptr(x), _ptr(codes), _ptr(scales),
                                   _ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(a), _ptr(b),
                                   _ptr(workspace), ws_bytes, _stream(stream)), "gdn_mx_in_proj")
+
+    def mx_in_proj_lora_workspace_bytes(self, n_tok, hidden, rank, with_z=True):
+        lib = load_library()
+        n = ctypes.c_size_t()
+        _check(lib.gdn_mx_in_proj_lora_workspace_bytes(self._h, n_tok, hidden, rank, int(with_z),
+                                                       ctypes.byref(n)),
+               "gdn_mx_in_proj_lora_workspace_bytes")
+        return n.value
+
+    def mx_in_proj_lora(self, x, codes, scales, lora_a, lora_b, lora_scale, token_adapter, q, k, v, a,
+                        b, z=None, workspace=None, stream=None):
+        """gdn_mx_in_proj_lora: mx_in_proj with a low-rank adapter per token (see
+        mx_proj_lora); the gates' logits get theirs before the activation."""
+        lib = _lib or load_library()
+        n_tok, hidden = int(x.shape[0]), int(x.shape[1])
+        h_v, kw, vw, io = self.desc.h_v, self._k_width, self._v_width, self.io_torch
+        n_out = self.c_conv + (0 if z is None else vw) + 2 * h_v
+        _need(x, "x", n_tok * hidden, torch.bfloat16)
+        _need(codes, "codes", n_out * hidden // 2, torch.uint8)
+        _need(scales, "scales", n_out * hidden // GDN_MX_GROUP, torch.uint8)
+        if not _hold(n_tok * kw, io, q, k):
+            _need(q, "q", n_tok * kw, io)
+            _need(k, "k", n_tok * kw, io)
+        if not _hold(n_tok * vw, io, v, v if z is None else z):
+            _need(v, "v", n_tok * vw, io)
+            if z is not None:
+                _need(z, "z", n_tok * vw, io)
+        if not _hold(n_tok * h_v, torch.float32, a, b):
+            _need(a, "a", n_tok * h_v, torch.float32)
+            _need(b, "b", n_tok * h_v, torch.float32)
+        n, rank = _lora_args(lora_a, lora_b, lora_scale, token_adapter, n_tok, hidden, n_out)
+        _on_current_device(q, lora_a, token_adapter)
+        ws, ws_bytes = _workspace(workspace)
+        _check(lib.gdn_mx_in_proj_lora(self._h, n_tok, hidden, x.data_ptr(), codes.data_ptr(),
+                                       scales.data_ptr(), n, rank, _ptr(lora_a), _ptr(lora_b),
+                                       _ptr(lora_scale), _ptr(token_adapter), _ptr(q), _ptr(k), _ptr(v),
+                                       _ptr(z), _ptr(a), _ptr(b), ws, ws_bytes, _stream(stream)),
+               "gdn_mx_in_proj_lora")
 
     def _prefill_args(self, n_seq, cu_seqlens, slot_ids, total_tokens, q, k, v, a, b, conv_w,
                       out):

@@ -447,6 +447,88 @@ gdn_status gdn_slot_copy(gdn_pool* pool, int32_t n, const int32_t* src_ids,
     });
 }
 
+gdn_status gdn_slot_reorder(gdn_pool* pool, int32_t n_req, int32_t width, const int32_t* slots,
+                            const int32_t* parents, int32_t* slots_out, void* stream) {
+    return guarded([&]() -> gdn_status {
+        if (!pool || n_req < 0 || width < 1) return GDN_ERR_INVALID_ARG;
+        if (n_req > 0 && (!slots || !parents || !slots_out)) return GDN_ERR_INVALID_ARG;
+        if (width > GDN_BEAM_MAX || (int64_t)n_req * width > 65535) return GDN_ERR_UNSUPPORTED;  // grid.y limit
+        if (n_req == 0) return GDN_OK;
+        hipStream_t s = as_stream(stream);
+        if (pool->desc.flags & GDN_VALIDATE) {
+            const gdn_status st = host_check_ids(slots, n_req * width, pool->desc.n_slots, s);
+            if (st != GDN_OK) return st;
+        }
+        return launch_slot_reorder(pool, n_req, width, slots, parents, slots_out, s) == hipSuccess ? GDN_OK
+                                                                                                  : GDN_ERR_HIP;
+    });
+}
+
+static gdn_status beam_args(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out) {
+    if (n_req < 0 || width < 1 || vocab < 1 || n_out < 1) return GDN_ERR_INVALID_ARG;
+    if (width > GDN_BEAM_MAX || n_out > GDN_BEAM_MAX || vocab > 1 << 30 || (int64_t)n_req * width > 1 << 20)
+        return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+gdn_status gdn_beam_select_workspace_bytes(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out,
+                                           size_t* bytes) {
+    const gdn_status st = beam_args(n_req, width, vocab, n_out);
+    if (st != GDN_OK) return st;
+    if (!bytes) return GDN_ERR_INVALID_ARG;
+    *bytes = beam_select_workspace_bytes(n_req, width, vocab, n_out);
+    return GDN_OK;
+}
+
+gdn_status gdn_beam_select(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype,
+                           const void* logits, int64_t ld, const float* scores, const uint8_t* finished,
+                           int32_t eos, int32_t* parents, int32_t* tokens, float* scores_out,
+                           uint8_t* finished_out, void* workspace, size_t workspace_bytes, void* stream) {
+    const gdn_status st = beam_args(n_req, width, vocab, n_out);
+    if (st != GDN_OK) return st;
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (finished && eos < 0) return GDN_ERR_INVALID_ARG;
+    if (n_req == 0) return GDN_OK;
+    if (!logits || !scores || !parents || !tokens || !scores_out) return GDN_ERR_INVALID_ARG;
+    if (!aligned(logits, dtype == GDN_BF16 ? 2 : 4) || !aligned(scores, 4) || !aligned(parents, 4) ||
+        !aligned(tokens, 4) || !aligned(scores_out, 4))
+        return GDN_ERR_INVALID_ARG;
+    if (n_req * width > 1 && ld < vocab) return GDN_ERR_INVALID_ARG;
+    if (workspace_bytes < beam_select_workspace_bytes(n_req, width, vocab, n_out) || !workspace)
+        return GDN_ERR_WORKSPACE;
+    if (!aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    return launch_beam_select(n_req, width, vocab, n_out, dtype, logits, ld, scores, finished, eos, parents,
+                              tokens, scores_out, finished_out, workspace, as_stream(stream)) == hipSuccess
+               ? GDN_OK
+               : GDN_ERR_HIP;
+}
+
+gdn_status gdn_batch_maps(gdn_pool* pool, int32_t n_seq, const int32_t* lens, int64_t max_tok,
+                          int32_t* cu_seqlens, int32_t* last_rows, int32_t* token_seq, const int32_t* past,
+                          int32_t* token_pos, const int32_t* adapter_ids, int32_t n_adapters,
+                          int32_t* token_adapter, int32_t ckpt_every, const int32_t* free_slots,
+                          int32_t n_free, int32_t* ckpt_offsets, int32_t* ckpt_slots, int32_t max_ckpt,
+                          void* stream) {
+    if (!pool || n_seq < 0 || max_tok < 0 || ckpt_every < 0 || !cu_seqlens) return GDN_ERR_INVALID_ARG;
+    if (n_seq > 0 && !lens) return GDN_ERR_INVALID_ARG;
+    if ((adapter_ids && n_adapters < 0) || (token_adapter && !adapter_ids && n_seq > 0)) return GDN_ERR_INVALID_ARG;
+    if (ckpt_every > 0 && (n_free < 0 || max_ckpt < 0 || !ckpt_offsets || (n_free > 0 && !free_slots) ||
+                           (max_ckpt > 0 && !ckpt_slots)))
+        return GDN_ERR_INVALID_ARG;
+    // sums of two counts that are cut off one past the limit stay in 32 bits
+    if (max_tok > INT32_MAX - 1) return GDN_ERR_UNSUPPORTED;
+    for (const void* p : {(const void*)lens, (const void*)cu_seqlens, (const void*)last_rows, (const void*)token_seq,
+                          (const void*)past, (const void*)token_pos, (const void*)adapter_ids,
+                          (const void*)token_adapter, (const void*)free_slots, (const void*)ckpt_offsets,
+                          (const void*)ckpt_slots})
+        if (!aligned(p, 4)) return GDN_ERR_INVALID_ARG;
+    return launch_batch_maps(pool, n_seq, lens, max_tok, cu_seqlens, last_rows, token_seq, past, token_pos,
+                             adapter_ids, n_adapters, token_adapter, ckpt_every, free_slots, n_free, ckpt_offsets,
+                             ckpt_slots, max_ckpt, as_stream(stream)) == hipSuccess
+               ? GDN_OK
+               : GDN_ERR_HIP;
+}
+
 static gdn_status ring_call(gdn_pool* pool, RingOp op, int32_t layer, int32_t n,
                             const int32_t* slot_ids, int32_t n_tok, const void* q, const void* k,
                             const void* v, const float* a, const float* b, const float* conv_w,
@@ -634,6 +716,20 @@ gdn_status gdn_mx_proj_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_ou
     return GDN_OK;
 }
 
+// The checks that both forms of a projection make; a single row's strides are set.
+static gdn_status mx_proj_operands(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t* ld_x,
+                                   const void* codes, const uint8_t* scales, gdn_dtype y_dtype, const void* y,
+                                   int64_t* ld_y) {
+    if (!x || !codes || !scales || !y) return GDN_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(y, elem_bytes(y_dtype))) return GDN_ERR_INVALID_ARG;
+    if (n_tok == 1) {   // a single row has no stride
+        *ld_x = n_in;
+        *ld_y = n_out;
+    }
+    if (*ld_x < n_in || *ld_x % 8 != 0 || *ld_y < n_out) return GDN_ERR_INVALID_ARG;
+    return *ld_x > 2 * GDN_MX_MAX_IN ? GDN_ERR_UNSUPPORTED : GDN_OK;
+}
+
 gdn_status gdn_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
                        const void* codes, const uint8_t* scales, gdn_dtype y_dtype, void* y, int64_t ld_y,
                        void* workspace, size_t /*workspace_bytes*/, void* stream) {
@@ -641,14 +737,8 @@ gdn_status gdn_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x
     if (st != GDN_OK) return st;
     if (!dtype_ok(y_dtype)) return GDN_ERR_INVALID_ARG;
     if (n_tok == 0) return GDN_OK;
-    if (!x || !codes || !scales || !y) return GDN_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(y, elem_bytes(y_dtype))) return GDN_ERR_INVALID_ARG;
-    if (n_tok == 1) {   // a single row has no stride
-        ld_x = n_in;
-        ld_y = n_out;
-    }
-    if (ld_x < n_in || ld_x % 8 != 0 || ld_y < n_out) return GDN_ERR_INVALID_ARG;
-    if (ld_x > 2 * GDN_MX_MAX_IN) return GDN_ERR_UNSUPPORTED;
+    st = mx_proj_operands(n_tok, n_in, n_out, x, &ld_x, codes, scales, y_dtype, y, &ld_y);
+    if (st != GDN_OK) return st;
     st = mx_workspace_ok(workspace);
     if (st != GDN_OK) return st;
     return launch_mx_proj(n_tok, n_in, n_out, x, ld_x, codes, scales, y_dtype, y, ld_y, as_stream(stream)) ==
@@ -668,6 +758,17 @@ gdn_status gdn_mx_in_proj_workspace_bytes(const gdn_pool* pool, int64_t n_tok, i
     return GDN_OK;
 }
 
+static gdn_status mx_in_proj_operands(const gdn_pool* pool, const void* x, const void* codes, const uint8_t* scales,
+                                      const void* q, const void* k, const void* v, const void* z, const float* a,
+                                      const float* b) {
+    if (!x || !codes || !scales || !q || !k || !v || !a || !b) return GDN_ERR_INVALID_ARG;
+    const size_t io = (size_t)pool->io_size;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(q, io) || !aligned(k, io) || !aligned(v, io) ||
+        !aligned(z, io) || !aligned(a, 4) || !aligned(b, 4))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
 gdn_status gdn_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
                           const void* codes, const uint8_t* scales, void* q, void* k, void* v, void* z,
                           float* a, float* b, void* workspace, size_t /*workspace_bytes*/, void* stream) {
@@ -676,14 +777,91 @@ gdn_status gdn_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, c
     gdn_status st = mx_proj_args(n_tok, hidden, n_out);
     if (st != GDN_OK) return st;
     if (n_tok == 0) return GDN_OK;
-    if (!x || !codes || !scales || !q || !k || !v || !a || !b) return GDN_ERR_INVALID_ARG;
-    const size_t io = (size_t)pool->io_size;
-    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(q, io) || !aligned(k, io) || !aligned(v, io) ||
-        !aligned(z, io) || !aligned(a, 4) || !aligned(b, 4))
-        return GDN_ERR_INVALID_ARG;
+    st = mx_in_proj_operands(pool, x, codes, scales, q, k, v, z, a, b);
+    if (st != GDN_OK) return st;
     st = mx_workspace_ok(workspace);
     if (st != GDN_OK) return st;
     return launch_mx_in_proj(pool, n_tok, hidden, x, codes, scales, q, k, v, z, a, b, as_stream(stream)) ==
+                   hipSuccess
+               ? GDN_OK
+               : GDN_ERR_HIP;
+}
+
+static gdn_status lora_rank_ok(int32_t rank) {
+    if (rank < 1) return GDN_ERR_INVALID_ARG;
+    return rank % 8 != 0 || rank > GDN_LORA_MAX_RANK ? GDN_ERR_UNSUPPORTED : GDN_OK;
+}
+
+static gdn_status lora_operands(int64_t n_tok, const LoraArgs& l, const void* workspace, size_t workspace_bytes) {
+    if (!l.a || !l.b || !l.scale || !l.ids) return GDN_ERR_INVALID_ARG;
+    if (!aligned(l.a, 16) || !aligned(l.b, 16) || !aligned(l.scale, 4) || !aligned(l.ids, 4)) return GDN_ERR_INVALID_ARG;
+    if (workspace_bytes < lora_workspace_bytes(n_tok, l.rank) || !workspace) return GDN_ERR_WORKSPACE;
+    return aligned(workspace, kAlign) ? GDN_OK : GDN_ERR_INVALID_ARG;
+}
+
+gdn_status gdn_mx_proj_lora_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out, int32_t rank,
+                                            size_t* bytes) {
+    gdn_status st = mx_proj_args(n_tok, n_in, n_out);
+    if (st == GDN_OK) st = lora_rank_ok(rank);
+    if (st != GDN_OK) return st;
+    if (!bytes) return GDN_ERR_INVALID_ARG;
+    *bytes = lora_workspace_bytes(n_tok, rank);
+    return GDN_OK;
+}
+
+gdn_status gdn_mx_proj_lora(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
+                            const void* codes, const uint8_t* scales, int32_t n_adapters, int32_t rank,
+                            const void* lora_a, const void* lora_b, const float* lora_scale,
+                            const int32_t* token_adapter, gdn_dtype y_dtype, void* y, int64_t ld_y,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    if (n_adapters < 0) return GDN_ERR_INVALID_ARG;
+    if (n_adapters == 0)
+        return gdn_mx_proj(n_tok, n_in, n_out, x, ld_x, codes, scales, y_dtype, y, ld_y, workspace,
+                           workspace_bytes, stream);
+    gdn_status st = mx_proj_args(n_tok, n_in, n_out);
+    if (st == GDN_OK) st = lora_rank_ok(rank);
+    if (st != GDN_OK) return st;
+    if (!dtype_ok(y_dtype)) return GDN_ERR_INVALID_ARG;
+    if (n_tok == 0) return GDN_OK;
+    const LoraArgs l{n_adapters, rank, lora_a, lora_b, lora_scale, token_adapter, static_cast<float*>(workspace)};
+    st = mx_proj_operands(n_tok, n_in, n_out, x, &ld_x, codes, scales, y_dtype, y, &ld_y);
+    if (st == GDN_OK) st = lora_operands(n_tok, l, workspace, workspace_bytes);
+    if (st != GDN_OK) return st;
+    return launch_mx_proj_lora(n_tok, n_in, n_out, x, ld_x, codes, scales, l, y_dtype, y, ld_y,
+                               as_stream(stream)) == hipSuccess
+               ? GDN_OK
+               : GDN_ERR_HIP;
+}
+
+gdn_status gdn_mx_in_proj_lora_workspace_bytes(const gdn_pool* pool, int64_t n_tok, int32_t hidden,
+                                               int32_t rank, int32_t with_z, size_t* bytes) {
+    if (!pool) return GDN_ERR_INVALID_ARG;
+    gdn_status st = mx_proj_args(n_tok, hidden, mx_in_proj_channels(pool, with_z != 0));
+    if (st == GDN_OK) st = lora_rank_ok(rank);
+    if (st != GDN_OK) return st;
+    if (!bytes) return GDN_ERR_INVALID_ARG;
+    *bytes = lora_workspace_bytes(n_tok, rank);
+    return GDN_OK;
+}
+
+gdn_status gdn_mx_in_proj_lora(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
+                               const void* codes, const uint8_t* scales, int32_t n_adapters, int32_t rank,
+                               const void* lora_a, const void* lora_b, const float* lora_scale,
+                               const int32_t* token_adapter, void* q, void* k, void* v, void* z, float* a,
+                               float* b, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!pool || n_adapters < 0) return GDN_ERR_INVALID_ARG;
+    if (n_adapters == 0)
+        return gdn_mx_in_proj(pool, n_tok, hidden, x, codes, scales, q, k, v, z, a, b, workspace, workspace_bytes,
+                              stream);
+    gdn_status st = mx_proj_args(n_tok, hidden, mx_in_proj_channels(pool, z != nullptr));
+    if (st == GDN_OK) st = lora_rank_ok(rank);
+    if (st != GDN_OK) return st;
+    if (n_tok == 0) return GDN_OK;
+    const LoraArgs l{n_adapters, rank, lora_a, lora_b, lora_scale, token_adapter, static_cast<float*>(workspace)};
+    st = mx_in_proj_operands(pool, x, codes, scales, q, k, v, z, a, b);
+    if (st == GDN_OK) st = lora_operands(n_tok, l, workspace, workspace_bytes);
+    if (st != GDN_OK) return st;
+    return launch_mx_in_proj_lora(pool, n_tok, hidden, x, codes, scales, l, q, k, v, z, a, b, as_stream(stream)) ==
                    hipSuccess
                ? GDN_OK
                : GDN_ERR_HIP;
@@ -710,7 +888,7 @@ const char* gdn_status_string(gdn_status status) {
         case GDN_ERR_INVALID_ARG: return "invalid argument";
         case GDN_ERR_UNSUPPORTED: return "unsupported shape or option";
         case GDN_ERR_BAD_INDEX: return "slot id out of range or repeated, or malformed cu_seqlens";
-        case GDN_ERR_WORKSPACE: return "prefill workspace too small";
+        case GDN_ERR_WORKSPACE: return "workspace too small";
         case GDN_ERR_HIP: return "HIP runtime error";
         case GDN_ERR_RING: return "a listed slot's verify ring is not empty (flush it first)";
         case GDN_ERR_HOST: return "host-side failure (host memory)";

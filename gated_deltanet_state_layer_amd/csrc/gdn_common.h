@@ -17,6 +17,7 @@ constexpr int kMaxVerifyTokens = 8;
 // Sticky error bits written to the pool's meta word.
 constexpr int kErrSlotRange = 1;
 constexpr int kErrSeqlens = 2;
+constexpr int kErrAdapter = 4;
 
 // ----------------------------------------------------------------- bf16 / io
 
@@ -111,6 +112,21 @@ hipError_t launch_slot_reset(const gdn_pool* pool, int32_t n, const int32_t* slo
                              hipStream_t stream);
 hipError_t launch_slot_copy(const gdn_pool* pool, int32_t n, const int32_t* src_ids,
                             const int32_t* dst_ids, hipStream_t stream);
+hipError_t launch_slot_reorder(const gdn_pool* pool, int32_t n_req, int32_t width, const int32_t* slots,
+                               const int32_t* parents, int32_t* slots_out, hipStream_t stream);
+// Beam selection.
+size_t beam_select_workspace_bytes(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out);
+hipError_t launch_beam_select(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype,
+                              const void* logits, int64_t ld, const float* scores, const uint8_t* finished,
+                              int32_t eos, int32_t* parents, int32_t* tokens, float* scores_out,
+                              uint8_t* finished_out, void* workspace, hipStream_t stream);
+// Maps of a batch.
+hipError_t launch_batch_maps(const gdn_pool* pool, int32_t n_seq, const int32_t* lens, int64_t max_tok,
+                             int32_t* cu_seqlens, int32_t* last_rows, int32_t* token_seq, const int32_t* past,
+                             int32_t* token_pos, const int32_t* adapter_ids, int32_t n_adapters,
+                             int32_t* token_adapter, int32_t ckpt_every, const int32_t* free_slots,
+                             int32_t n_free, int32_t* ckpt_offsets, int32_t* ckpt_slots, int32_t max_ckpt,
+                             hipStream_t stream);
 // More than 64 KiB of dynamic LDS has to be enabled per kernel (gfx950 has
 // 160 KiB per CU).  Done once per kernel and device: `done` holds one bit per
 // device id below 64 (set with release order once the attribute is in
@@ -202,6 +218,23 @@ hipError_t launch_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void
 hipError_t launch_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
                              const void* codes, const uint8_t* scales, void* q, void* k, void* v,
                              void* z, float* a, float* b, hipStream_t stream);
+// The same with low-rank adapters beside the weights.
+struct LoraArgs {
+    int32_t n_adapters, rank;
+    const void *a, *b;           // bf16 [n_adapters][rank][n_in], [n_adapters][n_out][rank]
+    const float* scale;          // [n_adapters]
+    const int32_t* ids;          // [n_tok]
+    float* h;                    // workspace
+};
+size_t lora_workspace_bytes(int64_t n_tok, int32_t rank);
+hipError_t launch_lora_shrink(int64_t n_tok, int32_t n_in, const void* x, int64_t ld_x, const LoraArgs& l,
+                              hipStream_t stream);
+hipError_t launch_mx_proj_lora(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
+                               const void* codes, const uint8_t* scales, const LoraArgs& l, gdn_dtype y_dtype,
+                               void* y, int64_t ld_y, hipStream_t stream);
+hipError_t launch_mx_in_proj_lora(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
+                                  const void* codes, const uint8_t* scales, const LoraArgs& l, void* q, void* k,
+                                  void* v, void* z, float* a, float* b, hipStream_t stream);
 size_t prefill_workspace_bytes(const gdn_pool* pool, int32_t n_seq, int64_t total_tokens,
                                int32_t chunk);
 // The static prefill scratch (kStaticScratchBytes on every device): its

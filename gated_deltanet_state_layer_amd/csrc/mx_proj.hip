@@ -10,6 +10,7 @@
 // of a group: next to one value 2^16 above the others, 88 % of the bf16 results
 // came out wrong.
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_common.h"
 #include "mfma_split.h"
@@ -116,6 +117,44 @@ __device__ __forceinline__ int offset_if(bool in, int offset) {
     return v;
 }
 
+// A low-rank adapter per token beside the weights: token t's h[t] (scale x A^T of
+// its adapter, fp32, ldh apart, zeros from rank on) times the rows of its
+// adapter's B is added to the sums.  MxNoLora: none, and no code for it.
+struct MxLora {
+    const float* h;
+    const uint16_t* b;   // [n_adapters][n_out][rank]
+    const int32_t* ids;  // [n_tok]
+    int n_adapters, rank, ldh;
+};
+struct MxNoLora {};
+
+__device__ __forceinline__ float dot8(u32x4 b, f32x4 h0, f32x4 h1, float s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(b[i] << 16), i < 2 ? h0[2 * i] : h1[2 * i - 4], s);
+        s = fmaf(__uint_as_float(b[i] & 0xffff0000u), i < 2 ? h0[2 * i + 1] : h1[2 * i - 3], s);
+    }
+    return s;
+}
+
+// What token t's adapter adds to channels n .. n+3.
+__device__ __forceinline__ f32x4 lora_at(const MxLora& l, int64_t t, int n, int n_out) {
+    f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int id = l.ids[t];
+    if ((unsigned)id >= (unsigned)l.n_adapters) return y;
+    const uint16_t* b = l.b + ((int64_t)id * n_out + n) * l.rank;
+    const float* h = l.h + t * l.ldh;
+    const int last = n_out - 1 - n;   // rows past the end repeat the last one
+#pragma unroll 2
+    for (int r = 0; r < l.rank; r += 8) {
+        const f32x4 h0 = *reinterpret_cast<const f32x4*>(h + r), h1 = *reinterpret_cast<const f32x4*>(h + r + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            y[j] = dot8(*reinterpret_cast<const u32x4*>(b + min(j, last) * l.rank + r), h0, h1, y[j]);
+    }
+    return y;
+}
+
 struct MxIn {
     const uint16_t* x;
     const uint8_t *codes, *scales;
@@ -153,8 +192,8 @@ struct SkinnyShape {
     static_assert((R == 4 || R % 16 == 0) && NC <= 4 && D <= 2 && kAhead < 64, "the schedule");
 };
 
-template <typename T, int R, int NC, int D>
-__global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, MxOut o, int c0, int cols) {
+template <typename T, int R, int NC, int D, typename L>
+__global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, MxOut o, int c0, int cols, L lora) {
     using S = SkinnyShape<R, NC, D>;
     constexpr int NT = S::NT;
     extern __shared__ __align__(16) uint8_t lds[];
@@ -267,6 +306,7 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
 #pragma unroll
         for (int w = 0; w < kSkinnyWaves; ++w)
             y += *reinterpret_cast<const f32x4*>(&red[(w * R + t) * S::LD + c]);
+        if constexpr (std::is_same_v<L, MxLora>) y += lora_at(lora, t0 + t, n0 + c, p.n_out);
         mx_put4<T>(o, t0 + t, n0 + c, y);
     }
 }
@@ -311,8 +351,60 @@ struct TileShape {
     static_assert(WAVES * 16 * kRow <= kScale && kBytes <= 160 * 1024, "fits");
 };
 
-template <typename T, int NC>
-__global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut o, int tiles_t, int n_end) {
+// Adds the adapters' share to the sums of a wave's 16 tokens by 16 NC channels:
+// lane (q, m) holds channels c * 16 + 4q .. of token m.  Sixteen ranks are two
+// MFMAs of 32: the three bf16 pieces of h, which hold its 24 bits, two to the first
+// and one to the second, beside the same rows of B.  One pass per adapter among the
+// 16 tokens; a token takes its own alone, summed apart from the others', so that
+// its result does not depend on theirs.
+template <int NC>
+__device__ __forceinline__ void lora_tile(const MxLora& l, int64_t tok, int64_t n_tok, int n0, int n_out, int n_end,
+                                          f32x4 (&acc)[NC]) {
+    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
+    const int id = tok < n_tok ? l.ids[tok] : -1;
+    const bool has = (unsigned)id < (unsigned)l.n_adapters;
+    uint64_t left = __ballot(has);
+    while (left) {
+        const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        const bool mine = has && id == cur;
+        left &= ~__ballot(mine);
+        f32x4 d[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) d[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const uint16_t* b = l.b + (int64_t)cur * n_out * l.rank;
+#pragma unroll 1
+        for (int r0 = 0; r0 < l.rank; r0 += 16) {
+            const int r = r0 + 8 * (q & 1);
+            bf16x8 h1, h2;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float x = mine ? l.h[tok * l.ldh + r + j] : 0.f;
+                const __bf16 hi = (__bf16)x;
+                const float e = x - (float)hi;
+                // an infinity has no further pieces
+                const __bf16 mid = (__bf16)(fabsf(e) <= 3.0e38f ? e : 0.f);
+                const float f = e - (float)mid;
+                h1[j] = q < 2 ? hi : mid;
+                h2[j] = q < 2 && fabsf(f) <= 3.0e38f ? (__bf16)f : (__bf16)0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int n = n0 + c * 16 + m;
+                u32x4 w = u32x4{0u, 0u, 0u, 0u};
+                if (n < n_end && r < l.rank) w = *reinterpret_cast<const u32x4*>(b + (int64_t)n * l.rank + r);
+                d[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), h1, d[c], 0, 0, 0);
+                d[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), h2, d[c], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[c][j] = mine ? acc[c][j] + d[c][j] : acc[c][j];
+    }
+}
+
+template <typename T, int NC, typename L>
+__global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut o, int tiles_t, int n_end, L lora) {
     using S = TileShape<NC>;
     constexpr int NT = S::NT;
     extern __shared__ __align__(16) uint8_t lds[];
@@ -518,6 +610,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut 
     uint8_t* eb = lds + wave * (16 * S::kRow);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+        if constexpr (std::is_same_v<L, MxLora>)
+            lora_tile<NC>(lora, tw + t * 16 + m, p.n_tok, nw, p.n_out, n_end, acc[t]);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             *reinterpret_cast<f32x4*>(eb + m * S::kRow + (c * 16 + 4 * q) * 4) = acc[t][c];
@@ -560,63 +654,69 @@ bool fits(const void* p, int64_t ld, int elem, int vec) {
     return reinterpret_cast<uintptr_t>(p) % (vec * elem) == 0 && ld % vec == 0;
 }
 
-template <typename T, int R, int NC, int D = 2>
-hipError_t skinny(const MxIn& p, const MxOut& o, const MxLaunch& l, hipStream_t stream) {
+template <typename T, int R, int NC, int D = 2, typename L>
+hipError_t skinny(const MxIn& p, const MxOut& o, const MxLaunch& l, const L& lora, hipStream_t stream) {
     constexpr int lds = SkinnyShape<R, NC, D>::kBytes;
     static_assert(lds <= 160 * 1024, "fits");
     if (lds > 65536) {
         static std::atomic<uint64_t> done{0};
-        const hipError_t e = allow_dynamic_lds(&mx_skinny_kernel<T, R, NC, D>, lds, &done);
+        const hipError_t e = allow_dynamic_lds(&mx_skinny_kernel<T, R, NC, D, L>, lds, &done);
         if (e != hipSuccess) return e;
     }
     const int cols = (l.c1 - l.c0 + 16 * NC - 1) / (16 * NC);
-    hipLaunchKernelGGL((mx_skinny_kernel<T, R, NC, D>), dim3((unsigned)l.workgroups), dim3(kSkinnyThreads), lds, stream,
-                       p, o, l.c0, cols);
+    hipLaunchKernelGGL((mx_skinny_kernel<T, R, NC, D, L>), dim3((unsigned)l.workgroups), dim3(kSkinnyThreads), lds,
+                       stream, p, o, l.c0, cols, lora);
     return hipGetLastError();
 }
 
-template <typename T, int NC>
-hipError_t tile(const MxIn& p, const MxOut& o, const MxLaunch& l, hipStream_t stream) {
+template <typename T, int NC, typename L>
+hipError_t tile(const MxIn& p, const MxOut& o, const MxLaunch& l, const L& lora, hipStream_t stream) {
     using S = TileShape<NC>;
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_dynamic_lds(&mx_tile_kernel<T, NC>, S::kBytes, &done);
+    const hipError_t e = allow_dynamic_lds(&mx_tile_kernel<T, NC, L>, S::kBytes, &done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((mx_tile_kernel<T, NC>), dim3((unsigned)l.workgroups), dim3(kTileThreads), S::kBytes, stream, p,
-                       o, (int)((p.n_tok + kTileTokens - 1) / kTileTokens), l.c1);
+    hipLaunchKernelGGL((mx_tile_kernel<T, NC, L>), dim3((unsigned)l.workgroups), dim3(kTileThreads), S::kBytes, stream,
+                       p, o, (int)((p.n_tok + kTileTokens - 1) / kTileTokens), l.c1, lora);
     return hipGetLastError();
 }
 
-template <typename T>
-hipError_t launch_one(const MxIn& p, const MxOut& o, const MxLaunch& l, hipStream_t stream) {
-    if (l.tile) return l.channels == 192 ? tile<T, 6>(p, o, l, stream) : tile<T, 4>(p, o, l, stream);
+template <typename T, typename L>
+hipError_t launch_one(const MxIn& p, const MxOut& o, const MxLaunch& l, const L& lora, hipStream_t stream) {
+    if (l.tile) return l.channels == 192 ? tile<T, 6>(p, o, l, lora, stream) : tile<T, 4>(p, o, l, lora, stream);
     switch (l.tokens * 256 + l.channels) {
-        case 4 * 256 + 16: return skinny<T, 4, 1>(p, o, l, stream);
-        case 4 * 256 + 32: return skinny<T, 4, 2>(p, o, l, stream);
-        case 16 * 256 + 16: return skinny<T, 16, 1>(p, o, l, stream);
-        case 16 * 256 + 32: return skinny<T, 16, 2>(p, o, l, stream);
-        case 16 * 256 + 64: return skinny<T, 16, 4>(p, o, l, stream);
-        case 32 * 256 + 64: return skinny<T, 32, 4, 1>(p, o, l, stream);
+        case 4 * 256 + 16: return skinny<T, 4, 1>(p, o, l, lora, stream);
+        case 4 * 256 + 32: return skinny<T, 4, 2>(p, o, l, lora, stream);
+        case 16 * 256 + 16: return skinny<T, 16, 1>(p, o, l, lora, stream);
+        case 16 * 256 + 32: return skinny<T, 16, 2>(p, o, l, lora, stream);
+        case 16 * 256 + 64: return skinny<T, 16, 4>(p, o, l, lora, stream);
+        case 32 * 256 + 64: return skinny<T, 32, 4, 1>(p, o, l, lora, stream);
         default: return hipErrorInvalidValue;   // a shape without a kernel
     }
 }
 
-template <typename T>
-hipError_t launch_typed(const MxIn& p, const MxOut& o, hipStream_t stream) {
+template <typename T, typename L>
+hipError_t launch_typed(const MxIn& p, const MxOut& o, const L& lora, hipStream_t stream) {
     const MxPlan plan = mx_plan(p.n_tok, p.n_in, p.n_out);
     for (int i = 0; i < plan.n; ++i) {
-        const hipError_t e = launch_one<T>(p, o, plan.launch[i], stream);
+        const hipError_t e = launch_one<T>(p, o, plan.launch[i], lora, stream);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
-}  // namespace
+template <typename L>
+hipError_t launch_any(gdn_dtype out, const MxIn& p, const MxOut& o, const L& lora, hipStream_t stream) {
+    return out == GDN_BF16 ? launch_typed<uint16_t>(p, o, lora, stream) : launch_typed<float>(p, o, lora, stream);
+}
 
-hipError_t launch_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
-                          const void* codes, const uint8_t* scales, gdn_dtype y_dtype, void* y,
-                          int64_t ld_y, hipStream_t stream) {
-    const MxIn p{static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(codes), scales,
-                 n_tok, ld_x, n_in, n_out};
+hipError_t launch_with(gdn_dtype out, const MxIn& p, const MxOut& o, const LoraArgs& l, hipStream_t stream) {
+    const hipError_t e = launch_lora_shrink(p.n_tok, p.n_in, p.x, p.ld_x, l, stream);
+    if (e != hipSuccess) return e;
+    const MxLora lora{l.h, static_cast<const uint16_t*>(l.b), l.ids, l.n_adapters, l.rank, (l.rank + 15) / 16 * 16};
+    return launch_any(out, p, o, lora, stream);
+}
+
+MxOut proj_out(int32_t n_out, gdn_dtype y_dtype, void* y, int64_t ld_y) {
     MxOut o{};
     o.seg[0] = y;
     o.ld[0] = ld_y;
@@ -625,13 +725,10 @@ hipError_t launch_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void
     const int elem = y_dtype == GDN_BF16 ? 2 : 4;
     o.vec4 = n_out % 4 == 0 && fits(y, ld_y, elem, 4);
     o.vec16 = n_out % (16 / elem) == 0 && fits(y, ld_y, elem, 16 / elem);
-    return y_dtype == GDN_BF16 ? launch_typed<uint16_t>(p, o, stream)
-                               : launch_typed<float>(p, o, stream);
+    return o;
 }
 
-hipError_t launch_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
-                             const void* codes, const uint8_t* scales, void* q, void* k, void* v,
-                             void* z, float* a, float* b, hipStream_t stream) {
+MxOut in_proj_out(const gdn_pool* pool, void* q, void* k, void* v, void* z, float* a, float* b) {
     const PoolView& P = pool->view;
     const int hkd = P.h_k * P.d, hvd = P.h_v * P.d;
     MxOut o{};
@@ -651,10 +748,43 @@ hipError_t launch_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden
     o.b = b;
     o.h_v = P.h_v;
     o.n_out = end + 2 * P.h_v;
+    return o;
+}
+
+}  // namespace
+
+hipError_t launch_mx_proj(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
+                          const void* codes, const uint8_t* scales, gdn_dtype y_dtype, void* y,
+                          int64_t ld_y, hipStream_t stream) {
+    const MxIn p{static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(codes), scales,
+                 n_tok, ld_x, n_in, n_out};
+    return launch_any(y_dtype, p, proj_out(n_out, y_dtype, y, ld_y), MxNoLora{}, stream);
+}
+
+hipError_t launch_mx_proj_lora(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
+                               const void* codes, const uint8_t* scales, const LoraArgs& l, gdn_dtype y_dtype,
+                               void* y, int64_t ld_y, hipStream_t stream) {
+    const MxIn p{static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(codes), scales,
+                 n_tok, ld_x, n_in, n_out};
+    return launch_with(y_dtype, p, proj_out(n_out, y_dtype, y, ld_y), l, stream);
+}
+
+hipError_t launch_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
+                             const void* codes, const uint8_t* scales, void* q, void* k, void* v,
+                             void* z, float* a, float* b, hipStream_t stream) {
+    const MxOut o = in_proj_out(pool, q, k, v, z, a, b);
     const MxIn p{static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(codes), scales,
                  n_tok, hidden, hidden, o.n_out};
-    return pool->desc.io_dtype == GDN_BF16 ? launch_typed<uint16_t>(p, o, stream)
-                                           : launch_typed<float>(p, o, stream);
+    return launch_any(pool->desc.io_dtype, p, o, MxNoLora{}, stream);
+}
+
+hipError_t launch_mx_in_proj_lora(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
+                                  const void* codes, const uint8_t* scales, const LoraArgs& l, void* q, void* k,
+                                  void* v, void* z, float* a, float* b, hipStream_t stream) {
+    const MxOut o = in_proj_out(pool, q, k, v, z, a, b);
+    const MxIn p{static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(codes), scales,
+                 n_tok, hidden, hidden, o.n_out};
+    return launch_with(pool->desc.io_dtype, p, o, l, stream);
 }
 
 }  // namespace gdn

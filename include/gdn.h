@@ -83,7 +83,7 @@ typedef int32_t gdn_status;
 #define GDN_ERR_INVALID_ARG (-1) /* null pointer, bad size or range */
 #define GDN_ERR_UNSUPPORTED (-2) /* shape outside the compiled kernels */
 #define GDN_ERR_BAD_INDEX (-3)   /* GDN_VALIDATE: slot id out of range or repeated */
-#define GDN_ERR_WORKSPACE (-4)   /* prefill workspace too small */
+#define GDN_ERR_WORKSPACE (-4)   /* workspace too small */
 #define GDN_ERR_HIP (-5)         /* a HIP runtime call failed */
 #define GDN_ERR_RING (-6)        /* GDN_VALIDATE: a listed slot's verify ring is not empty */
 #define GDN_ERR_HOST (-7)        /* host-side failure (e.g. GDN_VALIDATE cannot allocate its host copies) */
@@ -151,6 +151,91 @@ gdn_status gdn_slot_reset(gdn_pool* pool, int32_t n, const int32_t* slot_ids, vo
  * call (else the copies race; GDN_VALIDATE rejects it). */
 gdn_status gdn_slot_copy(gdn_pool* pool, int32_t n, const int32_t* src_ids, const int32_t* dst_ids,
                          void* stream);
+
+/* Beam search: reorder the states of n_req requests of `width` beams each (1 to
+ * GDN_BEAM_MAX) after a selection.
+ *   slots      device int32 [n_req][width]: the slot of each beam; a negative id
+ *              marks a padding beam, whose state is neither read nor written
+ *   parents    device int32 [n_req][width]: beam i of a request continues its
+ *              beam parents[i]; an id outside 0..width-1 marks a beam that
+ *              continues none
+ *   slots_out  device int32 [n_req][width]: afterwards slot slots_out[r][i]
+ *              holds, bit for bit, the state, conv window and verify ring of
+ *              every layer that slot slots[r][parents[r][i]] held
+ * slots_out[r] is a permutation of slots[r].  The first child of a beam keeps
+ * its slot; every other beam takes, in increasing order, the slot of a beam
+ * without children, in increasing order.  Only these are copied (none for a beam
+ * without a parent, whose slot keeps what it held).  slots_out may be slots;
+ * otherwise the two must not overlap.  Slots must be distinct within a call
+ * (GDN_VALIDATE rejects repeated slots and slots >= n_slots); a copy that would
+ * touch a slot >= n_slots is skipped and sets the sticky error word. */
+#define GDN_BEAM_MAX 64
+gdn_status gdn_slot_reorder(gdn_pool* pool, int32_t n_req, int32_t width, const int32_t* slots,
+                            const int32_t* parents, int32_t* slots_out, void* stream);
+
+/* Beam search: the best n_out continuations (1 to GDN_BEAM_MAX) of each request's
+ * `width` beams (1 to GDN_BEAM_MAX) over a vocabulary, beam b with token v being worth
+ *     scores[b] + logits[b][v] - log(sum over u of exp(logits[b][u])).
+ *   logits        device dtype [n_req * width][vocab], ld elements between rows
+ *                 (at least vocab; not read for a single row), aligned to the
+ *                 element; -infinity or NaN: the token is ruled out, +infinity
+ *                 counts as the largest finite value
+ *   scores        device fp32 [n_req][width]; a beam whose score is not finite
+ *                 has no continuations
+ *   finished      device bytes [n_req][width], or NULL: a beam with a nonzero
+ *                 byte has one continuation, the token eos at its own score
+ *   parents       device int32 [n_req][n_out]: the beam continued
+ *   tokens        device int32 [n_req][n_out]
+ *   scores_out    device fp32 [n_req][n_out], rounded once
+ *   finished_out  device bytes [n_req][n_out], or NULL: 1 where the beam
+ *                 continued was finished or the token is eos (a negative eos
+ *                 matches no token; finished must then be NULL)
+ *   workspace     device, >= gdn_beam_select_workspace_bytes, 256-byte aligned
+ * Sorted by falling score; of equal scores the lower beam comes first, then the
+ * larger logit, then the lower token.  Sums and scores are held in 64 bits, so the
+ * order is that of the exact scores to about 1e-11.  With fewer continuations
+ * than n_out the rest gets parent and token -1, score -infinity, finished 0.
+ * No two of the outputs may overlap, nor an output an input. */
+gdn_status gdn_beam_select_workspace_bytes(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out,
+                                           size_t* bytes);
+gdn_status gdn_beam_select(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype,
+                           const void* logits, int64_t ld, const float* scores, const uint8_t* finished,
+                           int32_t eos, int32_t* parents, int32_t* tokens, float* scores_out,
+                           uint8_t* finished_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The maps of a batch from its requests' lengths, on the device: the arrays that
+ * prefill, its checkpoints and the projections with adapters take.
+ *   lens           device int32 [n_seq]: tokens of each request in this batch
+ *                  (0: none; negative counts as 0 and sets the sticky error word)
+ *   max_tok        tokens the per-token arrays have room for; the tokens past
+ *                  that are dropped and set the sticky error word
+ *   cu_seqlens     device int32 [n_seq+1]: starts of the requests' tokens
+ *   last_rows      device int32 [n_seq], or NULL: row of each request's last token
+ *                  (-1 for none)
+ *   token_seq      device int32 [max_tok], or NULL: request of each token
+ *   past           device int32 [n_seq], or NULL (0): tokens before this batch
+ *   token_pos      device int32 [max_tok], or NULL: past + index in the batch
+ *   adapter_ids    device int32 [n_seq], or NULL; negative: no adapter
+ *   n_adapters     ids from here on count as none and set the sticky error word
+ *   token_adapter  device int32 [max_tok], or NULL (needs adapter_ids): adapter of
+ *                  each token, -1 for none
+ *   ckpt_every     tokens between state checkpoints, or 0 (the rest is then not
+ *                  looked at)
+ *   ckpt_offsets   device int32 [n_seq+1]: request j owns the floor(tokens /
+ *                  ckpt_every) checkpoint rows from ckpt_offsets[j]
+ *   free_slots     device int32 [n_free]: slots to use, in order
+ *   ckpt_slots     device int32 [max_ckpt]: row i gets free_slots[i], or -1 (not
+ *                  stored) behind the last free slot and behind the last row.
+ *                  Rows past max_ckpt are dropped: ckpt_offsets ends there
+ * Per-token rows behind the last token are set to -1.  The pool supplies the error
+ * word (bits 1 and 2 of gdn_pool_error).  max_tok and every count fit 31 bits, and
+ * past + tokens should. */
+gdn_status gdn_batch_maps(gdn_pool* pool, int32_t n_seq, const int32_t* lens, int64_t max_tok,
+                          int32_t* cu_seqlens, int32_t* last_rows, int32_t* token_seq, const int32_t* past,
+                          int32_t* token_pos, const int32_t* adapter_ids, int32_t n_adapters,
+                          int32_t* token_adapter, int32_t ckpt_every, const int32_t* free_slots,
+                          int32_t n_free, int32_t* ckpt_offsets, int32_t* ckpt_slots, int32_t max_ckpt,
+                          void* stream);
 
 /* One decode token for each of n entries; entry i reads and writes slot
  * slot_ids[i] of layer `layer` (baseRT issue #31, "Why this looks tractable":
@@ -438,9 +523,44 @@ gdn_status gdn_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, c
                           const void* codes, const uint8_t* scales, void* q, void* k, void* v, void* z,
                           float* a, float* b, void* workspace, size_t workspace_bytes, void* stream);
 
+/* gdn_mx_proj and gdn_mx_in_proj with a low-rank adapter per token beside the
+ * shared weights: with i = token_adapter[t],
+ *     y[t] = x[t] W^T + lora_scale[i] (x[t] A_i^T) B_i^T
+ * and y[t] = x[t] W^T for tokens without an adapter (any id outside
+ * 0..n_adapters-1); the gates a, b of the in-projection get theirs before the
+ * activation.  fp32 accumulation, one rounding at the end.  A token's result
+ * does not depend on which adapters the other tokens have.
+ *   lora_a         device bf16 [n_adapters][rank][n_in], 16-byte aligned
+ *   lora_b         device bf16 [n_adapters][n_out][rank], 16-byte aligned; n_out
+ *                  rows as W has
+ *   lora_scale     device fp32 [n_adapters]
+ *   token_adapter  device int32 [n_tok]
+ *   rank           a multiple of 8 up to GDN_LORA_MAX_RANK (UNSUPPORTED otherwise;
+ *                  smaller ranks are padded with zeros)
+ *   workspace      device, >= the workspace bytes, 256-byte aligned; scratch only
+ * Without adapters (n_adapters 0) the call is gdn_mx_proj / gdn_mx_in_proj and the
+ * adapters' arguments are not looked at.  Infinite adapter weights make the
+ * results of their own tokens infinite or NaN. */
+#define GDN_LORA_MAX_RANK 128
+gdn_status gdn_mx_proj_lora_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out, int32_t rank,
+                                            size_t* bytes);
+gdn_status gdn_mx_proj_lora(int64_t n_tok, int32_t n_in, int32_t n_out, const void* x, int64_t ld_x,
+                            const void* codes, const uint8_t* scales, int32_t n_adapters, int32_t rank,
+                            const void* lora_a, const void* lora_b, const float* lora_scale,
+                            const int32_t* token_adapter, gdn_dtype y_dtype, void* y, int64_t ld_y,
+                            void* workspace, size_t workspace_bytes, void* stream);
+gdn_status gdn_mx_in_proj_lora_workspace_bytes(const gdn_pool* pool, int64_t n_tok, int32_t hidden,
+                                               int32_t rank, int32_t with_z, size_t* bytes);
+gdn_status gdn_mx_in_proj_lora(const gdn_pool* pool, int64_t n_tok, int32_t hidden, const void* x,
+                               const void* codes, const uint8_t* scales, int32_t n_adapters, int32_t rank,
+                               const void* lora_a, const void* lora_b, const float* lora_scale,
+                               const int32_t* token_adapter, void* q, void* k, void* v, void* z, float* a,
+                               float* b, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then read and clear the sticky device error word
  * (0 = none; bit 0 = a slot id >= n_slots was skipped; bit 1 = a malformed
- * cu_seqlens was seen). */
+ * cu_seqlens or batch length was seen; bit 2 = an adapter id >= n_adapters was
+ * seen). */
 gdn_status gdn_pool_error(gdn_pool* pool, void* stream, int32_t* device_error);
 
 /* Static text for a status code. */
