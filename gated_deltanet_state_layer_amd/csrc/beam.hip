@@ -286,7 +286,10 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
             double sum = st.sum * exp64((double)st.c - (double)c);
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
-            const double norm = log(sum);   // apart from c: beside logits of 1e38 it would be lost
+            // One lane's sum for all: products contracted into the additions leave the
+            // lanes' a rounding apart, and equal logits need equal scores.  Apart from c,
+            // beside which it would be lost where logits reach 1e38.
+            const double norm = log(__builtin_bit_cast(double, read_lane(__builtin_bit_cast(uint64_t, sum), 0)));
             // The lists are sorted: their first keys come first, and few others pass.
             const uint64_t* from = keys + row * sh.splits * sh.n_out;
             Best best{0, held[wave], 0};

@@ -105,6 +105,14 @@ def test_ties_go_to_the_lower_token_and_beam(G, v, dtype):
     _check(G, y, torch.tensor([[0.0, -5.0]]), 30, name="zeros of both signs")
 
 
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_equal_logits_far_apart_in_a_long_row(G, seed):
+    """Equal bf16 logits among the best, from different stretches of a row."""
+    gen = _gen(seed)
+    x = _logits(gen, 32, 8, 40000, BF)
+    _check(G, x, -torch.rand(32, 8, generator=torch.Generator().manual_seed(seed)) * 8, 16)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("k", [1, 5, 64])
 def test_rising_and_falling_rows(G, dtype, k):
