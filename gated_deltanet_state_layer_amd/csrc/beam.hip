@@ -3,18 +3,18 @@
 //
 // Within a beam the order is that of the logits alone, so one pass over them finds
 // both a beam's best tokens and its sum; a second, small kernel puts the beams of a
-// request together.  A wave takes a stretch of a row: it sums exp(x - c), c a
-// logit near the largest so far, and holds the best 64 keys, sorted, one to a
-// lane, a key being logit and token.  An element is compared with the last key that
-// counts; the few that pass go through 64 places of LDS and are then sorted and
-// merged into the list.
+// request together.  A workgroup takes a stretch of a row.  Its waves sum
+// exp(x - c), c a logit near the largest so far, and compare each element with the
+// last key that counts, a key being logit and token.  The few that pass wait in
+// LDS; once there are 64, one wave sorts them, one to a lane, and merges them into
+// the sorted list of the best 64.
 //
 // Scores of different beams may lie closer than 32 bits resolve, and tokens are
 // whole numbers, right or wrong.  So exponentials and sums are fp64 here: the vector
-// units run them at fp32's rate, and a polynomial of degree 8 on |r| <= ln 2 / 2
-// (Chebyshev interpolation, 1.1e-12) keeps sums to about 1e-12.
+// units run them at fp32's rate.
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 
 #include "gdn_common.h"
 
@@ -22,28 +22,49 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kPer = 8, kStep = 64 * kPer;       // logits per lane and per wave of a step
+constexpr int kPer = 8, kStep = kThreads * kPer;  // logits per lane and per step of a workgroup
+constexpr int kHeld = 64 + 64 * kPer;            // keys of a wave that wait, 63 and a step's
+constexpr int kSide = 4;                         // exponentials side by side
 constexpr int kMaxSplits = 64;                   // a lane per stretch when they are put together
 constexpr int kMergeThreads = 512, kMergeWaves = kMergeThreads / 64;
 constexpr float kNone = -__builtin_inff();
 
-// exp(d) for -700 <= d <= 700 (below: exp(-700)).
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453;
+constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: a sum's low bits are its integer
+
+// exp(r) 2^n of N values side by side, |r| <= ln 2 / 2 or a little more, n in the low
+// bits of m.  The polynomial is the Chebyshev interpolation of degree 8 (1.1e-12).
+// The barriers keep the N chains of dependent products interleaved.
+template <int N>
+__device__ __forceinline__ void exp_scaled(const double (&r)[N], const double (&m)[N], double (&p)[N]) {
+    constexpr double kCoef[] = {2.4876070919998397e-05, 0.00019915868674658883, 0.001388882190450549,
+                                0.008333266094398913,   0.04166666688931224,    0.16666666891065027,
+                                0.4999999999980122,     0.9999999999797838,     1.0000000000000004};
+#pragma unroll
+    for (int k = 0; k < N; ++k) p[k] = kCoef[0];
+#pragma unroll
+    for (int j = 1; j < 9; ++j) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) p[k] = fma(p[k], r[k], kCoef[j]);
+        if constexpr (N > 1) __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        u32x2 bits = __builtin_bit_cast(u32x2, p[k]);
+        bits[1] += __builtin_bit_cast(u32x2, m[k])[0] << 20;
+        p[k] = __builtin_bit_cast(double, bits);
+    }
+}
+
+// exp(d), d <= 0; below -700 as there.
 __device__ __forceinline__ double exp64(double d) {
-    constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: the sum's low bits are the integer
     d = fmax(d, -700.0);
-    const double m = fma(d, 1.4426950408889634, kMagic), n = m - kMagic;
-    const double r = fma(n, -0.6931471805599453, d);
-    double p = 2.4876070919998397e-05;
-    p = fma(p, r, 0.00019915868674658883);
-    p = fma(p, r, 0.001388882190450549);
-    p = fma(p, r, 0.008333266094398913);
-    p = fma(p, r, 0.04166666688931224);
-    p = fma(p, r, 0.16666666891065027);
-    p = fma(p, r, 0.4999999999980122);
-    p = fma(p, r, 0.9999999999797838);
-    p = fma(p, r, 1.0000000000000004);
-    const uint64_t bits = __builtin_bit_cast(uint64_t, p) + ((uint64_t)(uint32_t)__builtin_bit_cast(uint64_t, m) << 52);
-    return __builtin_bit_cast(double, bits);
+    const double m[1] = {fma(d, kLog2e, kMagic)}, r[1] = {fma(m[0] - kMagic, -kLn2, d)};
+    double p[1];
+    exp_scaled(r, m, p);
+    return p[0];
 }
 
 // Order-preserving images of floating-point numbers; never 0 for numbers.
@@ -62,9 +83,10 @@ __device__ __forceinline__ double image_value(uint64_t k) {
     return __builtin_bit_cast(double, k ^ (k >> 63 ? (uint64_t)1 << 63 : ~(uint64_t)0));
 }
 
-// A logit and its token: larger logits first, of equal ones the lower token.  0: none.
+// A logit and its token: larger logits first, of equal ones the lower token.  0: none
+// (-infinity and NaN); +infinity counts as the largest finite value.
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t token) {
-    return x > kNone ? (uint64_t)image(x) << 32 | (uint32_t)~token : 0;
+    return x > kNone ? (uint64_t)image(fminf(x, FLT_MAX)) << 32 | (uint32_t)~token : 0;
 }
 
 // A continuation: its score's image (0: none), beam * 64 + place in the beam's list.
@@ -73,45 +95,93 @@ struct Entry {
     uint32_t tag;
 };
 
-__device__ __forceinline__ uint64_t across(uint64_t v, int mask) { return __shfl_xor(v, mask); }
-__device__ __forceinline__ Entry across(Entry v, int mask) {
-    return {__shfl_xor(v.score, mask), __shfl_xor(v.tag, mask)};
+// The value of lane (this ^ MASK).  Inside rows of 16 lanes by DPP, across them by the
+// row and half swaps: a sort of 64 keys makes no trip through LDS.
+template <int MASK>
+__device__ __forceinline__ uint32_t across(uint32_t v) {
+    static_assert(MASK > 0 && MASK < 64, "lanes");
+    if constexpr (MASK == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return (threadIdx.x & 32) ? r[0] : r[1];
+    } else if constexpr (MASK == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return (threadIdx.x & 16) ? r[0] : r[1];
+    } else if constexpr (MASK > 32) {
+        return across<32>(across<MASK - 32>(v));
+    } else if constexpr (MASK > 16) {
+        return across<16>(across<MASK - 16>(v));
+    } else if constexpr (MASK == 4) {
+        return across<7>(across<3>(v));
+    } else {
+        // quad permutes, mirror of half a row, turn by half a row, mirror of a row
+        constexpr int kCtrl = MASK == 1 ? 0xB1 : MASK == 2 ? 0x4E : MASK == 3 ? 0x1B : MASK == 7 ? 0x141
+                              : MASK == 8 ? 0x128 : 0x140;
+        static_assert(MASK == 1 || MASK == 2 || MASK == 3 || MASK == 7 || MASK == 8 || MASK == 15, "one step");
+        return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, false);
+    }
+}
+template <int MASK>
+__device__ __forceinline__ uint64_t across(uint64_t v) {
+    return (uint64_t)across<MASK>((uint32_t)(v >> 32)) << 32 | across<MASK>((uint32_t)v);
+}
+template <int MASK>
+__device__ __forceinline__ Entry across(Entry v) {
+    return {across<MASK>(v.score), across<MASK>(v.tag)};
 }
 __device__ __forceinline__ bool better(uint64_t a, uint64_t b) { return a > b; }
 __device__ __forceinline__ bool better(Entry a, Entry b) {
     return a.score > b.score || (a.score == b.score && a.tag < b.tag);
 }
 
-// One step of a sorting network: of lanes `mask` apart, the one with `first` keeps
-// the better value.
-template <typename V>
-__device__ __forceinline__ V exchange(V v, int mask, bool first) {
-    const V o = across(v, mask);
-    return better(o, v) == first ? o : v;
+// One step of a sorting network: of lanes MASK apart, the one whose bit BIT is clear
+// keeps the better value.
+template <int MASK, int BIT, typename V>
+__device__ __forceinline__ V exchange(V v) {
+    const V o = across<MASK>(v);
+    return better(o, v) == !(threadIdx.x & BIT) ? o : v;
+}
+
+// Sorts groups of 2 W lanes whose values rise and then fall, or the like.
+template <int W, typename V>
+__device__ __forceinline__ V settle(V v) {
+    if constexpr (W > 0) return settle<W / 2>(exchange<W, W>(v));
+    else return v;
 }
 
 // The wave's 64 values, best in lane 0.
-template <typename V>
+template <int W = 2, typename V>
 __device__ __forceinline__ V sort64(V v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int k = 2; k <= 64; k *= 2) {
-        v = exchange(v, k - 1, !(lane & (k / 2)));
-#pragma unroll
-        for (int j = k / 4; j > 0; j /= 2) v = exchange(v, j, !(lane & j));
-    }
-    return v;
+    v = settle<W / 4>(exchange<W - 1, W / 2>(v));
+    if constexpr (W < 64) return sort64<2 * W>(v);
+    else return v;
 }
 
 // The best 64 of two sorted lists, sorted.
 template <typename V>
 __device__ __forceinline__ V merge64(V a, V b) {
-    const int lane = threadIdx.x & 63;
-    const V o = across(b, 63);
-    V v = better(o, a) ? o : a;
-#pragma unroll
-    for (int j = 32; j > 0; j /= 2) v = exchange(v, j, !(lane & j));
-    return v;
+    const V o = across<63>(b);
+    return settle<32>(better(o, a) ? o : a);
+}
+
+// Sum and maximum over the wave, in every lane (the lanes' sums a rounding apart
+// where the compiler contracts a product into the first addition).
+template <int MASK = 1>
+__device__ __forceinline__ double all_sum(double v) {
+    v += __builtin_bit_cast(double, across<MASK>(__builtin_bit_cast(uint64_t, v)));
+    if constexpr (MASK < 32) return all_sum<2 * MASK>(v);
+    else return v;
+}
+template <int MASK = 1>
+__device__ __forceinline__ double all_max(double v) {
+    v = fmax(v, __builtin_bit_cast(double, across<MASK>(__builtin_bit_cast(uint64_t, v))));
+    if constexpr (MASK < 32) return all_max<2 * MASK>(v);
+    else return v;
+}
+template <int MASK = 1>
+__device__ __forceinline__ float all_max(float v) {
+    v = fmaxf(v, __uint_as_float(across<MASK>(__float_as_uint(v))));
+    if constexpr (MASK < 32) return all_max<2 * MASK>(v);
+    else return v;
 }
 
 __device__ __forceinline__ uint64_t read_lane(uint64_t v, int lane) {
@@ -119,141 +189,192 @@ __device__ __forceinline__ uint64_t read_lane(uint64_t v, int lane) {
            (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
-// A wave's own places of LDS: what its lanes wrote is there for all of them.
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
+// Logits i .. i+7 of a row as they are, -infinity behind its end.  Rows need not be
+// aligned.
+template <typename T> struct None;
+template <> struct None<float> { static constexpr float value = kNone; };
+template <> struct None<uint16_t> { static constexpr uint16_t value = 0xff80; };
 
-// The best keys of a stream: a sorted list in registers, and those that may join it
-// in LDS until there are 64.
-struct Best {
-    uint64_t list;
-    uint64_t* held;   // 128 places of the wave's own
-    int n;
-
-    __device__ __forceinline__ void join(int count) {
-        const int lane = threadIdx.x & 63;
-        wave_sync();
-        const uint64_t v = lane < count ? held[lane] : 0;
-        list = merge64(list, sort64(v));
-        wave_sync();
-    }
-    // Every lane brings a key; those of `mask` join.
-    __device__ __forceinline__ void add(uint64_t key, uint64_t mask) {
-        const int lane = threadIdx.x & 63;
-        if (mask >> lane & 1) held[n + __popcll(mask & (((uint64_t)1 << lane) - 1))] = key;
-        n += __popcll(mask);
-        if (n < 64) return;
-        join(64);
-        const uint64_t rest = lane < n - 64 ? held[64 + lane] : 0;
-        wave_sync();
-        held[lane] = rest;
-        wave_sync();
-        n -= 64;
-    }
-    __device__ __forceinline__ void finish() {
-        if (n > 0) join(n);
-        n = 0;
+template <typename T>
+struct Eight {
+    T v[kPer];
+    __device__ __forceinline__ void load(const T* row, int i, int vocab) {
+        if (i + kPer <= vocab) {
+            __builtin_memcpy(v, row + i, sizeof v);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) v[k] = i + k < vocab ? row[i + k] : None<T>::value;
+        }
     }
 };
 
-// Logits i .. i+7 of a row, -infinity behind its end; NaN reads as -infinity and
-// +infinity as the largest finite value.  Rows need not be aligned.
-template <typename T>
-__device__ __forceinline__ void load8(const T* row, int i, int vocab, float (&x)[kPer]) {
-    T raw[kPer];
-    if (i + kPer <= vocab) {
-        __builtin_memcpy(raw, row + i, sizeof raw);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) x[k] = Io<T>::load(raw, k);
-    } else {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) x[k] = i + k < vocab ? Io<T>::load(row, i + k) : kNone;
-    }
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) x[k] = x[k] != x[k] ? kNone : fminf(x[k], FLT_MAX);
-}
-
-// What a stretch of a row leaves: the logit c, the sum of exp(x - c), the keys.
+// What a stretch of a row leaves: the sum of exp(x - c), beside its best keys.
 struct Stretch {
-    double sum;
-    float c;
-    int pad;
+    double c, sum;
 };
 
 struct Shape {
-    int rows, width, vocab, n_out, splits, steps;   // steps of 512 logits to a stretch
+    int rows, width, vocab, n_out, splits, steps;   // steps of 2048 logits to a stretch
 };
 
-// One wave per stretch of a row.
+// Of equal groups of lanes the least of the groups' largest.
+template <int MASK = 1>
+__device__ __forceinline__ float reached(float top, int group) {
+    const float o = __uint_as_float(across<MASK>(__float_as_uint(top)));
+    top = MASK < group ? fmaxf(top, o) : fminf(top, o);
+    if constexpr (MASK < 32) return reached<2 * MASK>(top, group);
+    else return top;
+}
+
+// The larger of two numbers.  fmaxf takes a second instruction for NaN that signal.
+__device__ __forceinline__ float max_number(float a, float b) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
+// One workgroup per stretch of a row.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void beam_rows_kernel(Shape sh, const T* logits, int64_t ld, const float* scores,
                                                             const uint8_t* finished, Stretch* stats, uint64_t* keys) {
-    __shared__ uint64_t held[kWaves][128];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t item = (int64_t)blockIdx.x * kWaves + wave;
-    if (item >= (int64_t)sh.rows * sh.splits) return;
-    const int row = __builtin_amdgcn_readfirstlane((int)(item / sh.splits));
-    const int split = __builtin_amdgcn_readfirstlane((int)(item % sh.splits));
-    // a beam without continuations, or with one that needs no logits
-    if (!(fabsf(scores[row]) <= FLT_MAX) || (finished && finished[row])) return;
+    __shared__ u32x2 held[kWaves][kHeld];   // logit and token
+    __shared__ uint64_t list[64];
+    __shared__ int kept[2][kWaves];   // of even and odd steps: the last step's may still be read
+    __shared__ double sums[kWaves], tops[kWaves];
+    __shared__ float2 bounds[kWaves];
+    __shared__ float last;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = blockIdx.x / sh.splits, split = blockIdx.x % sh.splits;
     const T* x_row = logits + row * ld;
     const int begin = split * sh.steps * kStep, end = (int)min((int64_t)sh.vocab, (int64_t)begin + sh.steps * kStep);
-    float c = -FLT_MAX;
-    double sum = 0.0;
-    Best best{0, held[wave], 0};
-    float least = kNone;   // of the list's last key that counts
+    Eight<T> next;
+    next.load(x_row, begin + (int)threadIdx.x * kPer, sh.vocab);
+    // a beam without continuations, or with one that needs no logits
+    if (!(fabsf(scores[row]) <= FLT_MAX) || (finished && finished[row])) return;
+    // lanes to a part, for the first bound: parts of one wave, of all waves
+    const int alone = 64 >> (sh.n_out > 1 ? 32 - __builtin_clz(sh.n_out - 1) : 0);
+    const int group = min(64, alone * kWaves);
+    // Sums are of exp(x - c) with c = n ln 2, so that the exponent's integer takes c in;
+    // where |c| is large, x is first made x - base in fp32, exact where it counts.
+    float c = -FLT_MAX, base = c, least = kNone;   // least: the list's last key that counts
+    double shift = kMagic, sum = 0.0;
+    int n = 0, joins = 0, odd = 0;
     for (int i = begin; i < end; i += kStep) {
         float x[kPer];
-        const int at = i + lane * kPer;
-        load8(x_row, at, sh.vocab, x);
-        float top = x[0];
+        const int at = i + (int)threadIdx.x * kPer;
 #pragma unroll
-        for (int k = 1; k < kPer; ++k) top = fmaxf(top, x[k]);
-        if (__any(top > c + 600.0f)) {   // also the first time
-            float t = top;
+        for (int k = 0; k < kPer; ++k) x[k] = Io<T>::load(next.v, k);
+        if (i + kStep < end) next.load(x_row, at + kStep, sh.vocab);
+        // infinities and NaN are always above and always far
+        const float reach = c + 600.0f, bar = fminf(least, reach);
+        uint64_t above = 0;
 #pragma unroll
-            for (int d = 1; d < 64; d *= 2) t = fmaxf(t, __shfl_xor(t, d));
-            sum *= exp64((double)c - (double)t);
-            c = t;
-        }
+        for (int k = 0; k < kPer; ++k) above |= __ballot(!(x[k] <= bar));
+        if (above || i == begin) {
+            uint64_t far = 0;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) sum += exp64((double)x[k] - (double)c);
-        if (i == begin) {
-            // the n_out-th of the lanes' best keys: no fewer than n_out reach it
-            uint64_t mine = 0;
+            for (int k = 0; k < kPer; ++k) far |= __ballot(!(x[k] <= reach));
+            if (far || i == begin) {
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const uint64_t key = key_of(x[k], at + k);
-                mine = key > mine ? key : mine;
+                for (int k = 0; k < kPer; ++k) x[k] = x[k] != x[k] ? kNone : fminf(x[k], FLT_MAX);
+                float top = x[0];
+#pragma unroll
+                for (int k = 1; k < kPer; ++k) top = fmaxf(top, x[k]);
+                if (__any(top > reach)) {   // also the first time, unless nothing is above the lowest value
+                    const double old = (double)base + (kMagic - shift) * kLn2;
+                    c = all_max(top);
+                    const double ints = rint((double)c * kLog2e);
+                    base = fabsf(c) > 1e5f ? c : 0.0f;
+                    shift = fabsf(c) > 1e5f ? kMagic : kMagic - ints;
+                    sum *= exp64(old - ((double)base + (kMagic - shift) * kLn2));
+                }
+                if (i == begin) {
+                    // A bound that n_out logits of the step reach: of equal parts of the lanes,
+                    // no fewer than n_out, the least of the parts' largest; parts of all waves,
+                    // or of one where another has little.  Those equal to it may count, so
+                    // it is the number below it.
+                    const float own = reached(top, alone);
+                    top = reached(top, group);
+                    if (lane == 0) bounds[wave] = {top, own};
+                    __syncthreads();
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) top = fminf(top, bounds[w].x);
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, bounds[w].y);
+                    least = top > kNone ? image_value(image(top) - (top == 0.0f ? 2 : 1)) : kNone;
+                }
             }
-            const uint64_t bar = read_lane(sort64(mine), sh.n_out - 1);
-#pragma unroll 1
-            for (int k = 0; k < kPer; ++k) {
-                const uint64_t key = key_of(x[k], at + k);
-                best.add(key, __ballot(key && key >= bar));
-            }
-            best.finish();
-        } else if (__any(top > least)) {
-            // Later tokens lose against equal logits in the list; within the step
-            // the keys decide, so all of it is compared with the list from before.
-#pragma unroll 1
+            // Equal to the list's last is not enough: tokens are higher here.
+#pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 const uint64_t mask = __ballot(x[k] > least);
-                if (mask) best.add(key_of(x[k], at + k), mask);
+                if (mask) {
+                    const uint32_t to = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
+                    if (x[k] > least) held[wave][to] = u32x2{__float_as_uint(x[k]), (uint32_t)(at + k)};
+                    n += __popcll(mask);
+                }
             }
-        } else {
-            continue;
         }
-        const uint32_t last = (uint32_t)(read_lane(best.list, sh.n_out - 1) >> 32);
-        least = last ? image_value(last) : kNone;
-    }
-    best.finish();
+        odd ^= 1;
+        if (lane == 0) kept[odd][wave] = n;
+        if (base != 0.0f) {
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
-    if (lane == 0) stats[item] = {sum, c, 0};
-    if (lane < sh.n_out) keys[item * sh.n_out + lane] = best.list;
+            for (int k = 0; k < kPer; ++k) x[k] = x[k] - base;
+        }
+        const float low = c - base - 700.0f;
+#pragma unroll
+        for (int k0 = 0; k0 < kPer; k0 += kSide) {
+            double m[kSide], r[kSide], e[kSide];
+#pragma unroll
+            for (int k = 0; k < kSide; ++k) {
+                const double d = (double)max_number(x[k0 + k], low);
+                m[k] = fma(d, kLog2e, shift);
+                r[k] = fma(m[k] - shift, -kLn2, d);
+            }
+            exp_scaled(r, m, e);
+#pragma unroll
+            for (int k = 0; k < kSide; ++k) sum += e[k];
+        }
+        __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) total += kept[odd][w];
+        if (total < 64 && i != begin && i + kStep < end) continue;
+        // the waves take turns at the list
+        if (wave == joins % kWaves) {
+            uint64_t best = joins ? list[lane] : 0;
+            // place lane + 64 j of the waves' keys, one behind the other
+            for (int from = 0; from < total; from += 64) {
+                int w = 0, to = from + lane;
+                while (w < kWaves && to >= kept[odd][w]) to -= kept[odd][w++];
+                const u32x2 e = w < kWaves ? held[w][to] : u32x2{__float_as_uint(kNone), 0};
+                best = merge64(best, sort64(key_of(__uint_as_float(e[0]), e[1])));
+            }
+            list[lane] = best;
+            const uint32_t high = (uint32_t)(read_lane(best, sh.n_out - 1) >> 32);
+            if (lane == 0) last = high ? image_value(high) : kNone;
+        }
+        __syncthreads();
+        least = last;
+        n = 0;
+        ++joins;
+    }
+    sum = all_sum(sum);
+    if (lane == 0) {
+        tops[wave] = (double)base + (kMagic - shift) * kLn2;
+        sums[wave] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double m = tops[0], all = 0.0;
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) m = fmax(m, tops[w]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) all += sums[w] * exp64(tops[w] - m);
+        stats[blockIdx.x] = {m, all};
+    }
+    if (wave == 0 && lane < sh.n_out) keys[(int64_t)blockIdx.x * sh.n_out + lane] = list[lane];
 }
 
 // One workgroup per request: each wave puts the stretches of its beams together,
@@ -262,7 +383,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
                                                                   const float* scores, const uint8_t* finished, int eos,
                                                                   int32_t* parents, int32_t* tokens, float* scores_out,
                                                                   uint8_t* finished_out) {
-    __shared__ uint64_t held[kMergeWaves][128], l_score[kMergeWaves][64];
+    __shared__ uint64_t l_score[kMergeWaves][64];
     __shared__ uint32_t l_tag[kMergeWaves][64];
     __shared__ int32_t token[GDN_BEAM_MAX * GDN_BEAM_MAX];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -270,44 +391,38 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
     Entry mine{0, ~0u};
     for (int b = wave; b < sh.width; b += kMergeWaves) {
         const int64_t row = req * sh.width + b;
+        // all loads at once; what a beam without logits has there is not looked at
+        const int count = sh.splits * sh.n_out;
+        const uint64_t* from = keys + row * count;
+        const auto key_at = [&](int i) { return i < count ? from[i % sh.splits * sh.n_out + i / sh.splits] : 0; };
+        uint64_t key = key_at(lane);
+        const Stretch st = lane < sh.splits ? stats[row * sh.splits + lane] : Stretch{-HUGE_VAL, 0.0};
         const float base = scores[row];
+        const bool done = finished && finished[row];
         if (!(fabsf(base) <= FLT_MAX)) continue;
         Entry e{0, (uint32_t)(b * 64 + lane)};
-        if (finished && finished[row]) {
+        if (done) {
             if (lane == 0) {
                 e.score = image((double)base);
                 token[b * 64] = eos;
             }
         } else {
-            const Stretch st = lane < sh.splits ? stats[row * sh.splits + lane] : Stretch{0.0, -FLT_MAX, 0};
-            float c = st.c;
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) c = fmaxf(c, __shfl_xor(c, d));
-            double sum = st.sum * exp64((double)st.c - (double)c);
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
-            // One lane's sum for all: products contracted into the additions leave the
-            // lanes' a rounding apart, and equal logits need equal scores.  Apart from c,
-            // beside which it would be lost where logits reach 1e38.
+            const double c = all_max(st.c);
+            const double sum = all_sum(st.sum * exp64(st.c - c));
+            // One lane's sum for all: equal logits need equal scores.  Apart from c, beside
+            // which the logarithm would be lost where logits reach 1e38.
             const double norm = log(__builtin_bit_cast(double, read_lane(__builtin_bit_cast(uint64_t, sum), 0)));
             // The lists are sorted: their first keys come first, and few others pass.
-            const uint64_t* from = keys + row * sh.splits * sh.n_out;
-            Best best{0, held[wave], 0};
-            uint64_t bar = 0;
-            for (int i = 0; i < sh.splits * sh.n_out; i += 64) {
-                const int f = i + lane;
-                const uint64_t key =
-                    f < sh.splits * sh.n_out ? from[f % sh.splits * sh.n_out + f / sh.splits] : 0;
-                const uint64_t mask = __ballot(key > bar);
-                if (!mask) break;   // every list has a key here, and none further down is larger
-                best.add(key, mask);
-                best.finish();
-                bar = read_lane(best.list, sh.n_out - 1);
+            uint64_t best = sort64(key);
+            for (int i = 64; i < count; i += 64) {
+                key = key_at(i + lane);
+                if (!__any(key > read_lane(best, sh.n_out - 1))) break;   // every list has a key here: none further down is larger
+                best = merge64(best, sort64(key));
             }
-            if (best.list && lane < sh.n_out) {
+            if (best && lane < sh.n_out) {
                 e.score = image((double)base +
-                                (((double)image_value((uint32_t)(best.list >> 32)) - (double)c) - norm));
-                token[b * 64 + lane] = (int32_t)~(uint32_t)best.list;
+                                (((double)image_value((uint32_t)(best >> 32)) - c) - norm));
+                token[b * 64 + lane] = (int32_t)~(uint32_t)best;
             }
         }
         mine = merge64(mine, e);
@@ -331,7 +446,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
 // Stretches: enough waves for the card, at most a lane's worth, none empty.
 Shape beam_shape(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out) {
     const int rows = n_req * width, steps = (vocab + kStep - 1) / kStep;
-    const int want = std::max(1, std::min({kMaxSplits, steps, 8192 / std::max(1, rows)}));
+    const int want = std::max(1, std::min({kMaxSplits, steps, 2048 / std::max(1, rows)}));
     const int per = (steps + want - 1) / want;
     return {rows, width, vocab, n_out, (steps + per - 1) / per, per};
 }
@@ -354,7 +469,7 @@ hipError_t launch_beam_select(int32_t n_req, int32_t width, int32_t vocab, int32
     const Shape s = beam_shape(n_req, width, vocab, n_out);
     Stretch* stats = static_cast<Stretch*>(workspace);
     uint64_t* keys = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + stats_bytes(s));
-    const dim3 grid((unsigned)(((int64_t)s.rows * s.splits + kWaves - 1) / kWaves));
+    const dim3 grid((unsigned)(s.rows * s.splits));
     if (dtype == GDN_BF16)
         hipLaunchKernelGGL(beam_rows_kernel<uint16_t>, grid, dim3(kThreads), 0, stream, s,
                            static_cast<const uint16_t*>(logits), ld, scores, finished, stats, keys);

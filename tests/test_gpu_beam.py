@@ -102,6 +102,10 @@ def test_ties_go_to_the_lower_token_and_beam(G, v, dtype):
     _check(G, torch.zeros(1, 3, v, dtype=dtype, device="cuda"), torch.tensor([[-1.0, -1.0, 0.0]]), 20, name="equal")
     y = torch.zeros(1, 2, v, dtype=dtype, device="cuda")
     y[0, 0, ::2] = -0.0
+    z = -torch.rand(1, 2, v, device="cuda") - 0.1
+    z[0, 0, 3:9] = 0.0
+    z[0, 1, 5:33] = -0.0
+    _check(G, z.to(dtype), torch.tensor([[0.0, -5.0]]), 24, name="zeros on top")
     _check(G, y, torch.tensor([[0.0, -5.0]]), 30, name="zeros of both signs")
 
 
