@@ -823,7 +823,7 @@ gdn_status gdn_mx_proj_lora(int64_t n_tok, int32_t n_in, int32_t n_out, const vo
     if (st != GDN_OK) return st;
     if (!dtype_ok(y_dtype)) return GDN_ERR_INVALID_ARG;
     if (n_tok == 0) return GDN_OK;
-    const LoraArgs l{n_adapters, rank, lora_a, lora_b, lora_scale, token_adapter, static_cast<float*>(workspace)};
+    const LoraArgs l{n_adapters, rank, lora_a, lora_b, lora_scale, token_adapter, workspace};
     st = mx_proj_operands(n_tok, n_in, n_out, x, &ld_x, codes, scales, y_dtype, y, &ld_y);
     if (st == GDN_OK) st = lora_operands(n_tok, l, workspace, workspace_bytes);
     if (st != GDN_OK) return st;
@@ -857,7 +857,7 @@ gdn_status gdn_mx_in_proj_lora(const gdn_pool* pool, int64_t n_tok, int32_t hidd
     if (st == GDN_OK) st = lora_rank_ok(rank);
     if (st != GDN_OK) return st;
     if (n_tok == 0) return GDN_OK;
-    const LoraArgs l{n_adapters, rank, lora_a, lora_b, lora_scale, token_adapter, static_cast<float*>(workspace)};
+    const LoraArgs l{n_adapters, rank, lora_a, lora_b, lora_scale, token_adapter, workspace};
     st = mx_in_proj_operands(pool, x, codes, scales, q, k, v, z, a, b);
     if (st == GDN_OK) st = lora_operands(n_tok, l, workspace, workspace_bytes);
     if (st != GDN_OK) return st;

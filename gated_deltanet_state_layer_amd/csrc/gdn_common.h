@@ -224,7 +224,7 @@ struct LoraArgs {
     const void *a, *b;           // bf16 [n_adapters][rank][n_in], [n_adapters][n_out][rank]
     const float* scale;          // [n_adapters]
     const int32_t* ids;          // [n_tok]
-    float* h;                    // workspace
+    void* h;                     // workspace: s x A^T in pieces (see lora.hip)
 };
 size_t lora_workspace_bytes(int64_t n_tok, int32_t rank);
 hipError_t launch_lora_shrink(int64_t n_tok, int32_t n_in, const void* x, int64_t ld_x, const LoraArgs& l,

@@ -118,24 +118,18 @@ __device__ __forceinline__ int offset_if(bool in, int offset) {
 }
 
 // A low-rank adapter per token beside the weights: token t's h[t] (scale x A^T of
-// its adapter, fp32, ldh apart, zeros from rank on) times the rows of its
-// adapter's B is added to the sums.  MxNoLora: none, and no code for it.
+// its adapter, in three bf16 pieces by blocks of 16 ranks: see lora.hip) times the
+// rows of its adapter's B is added to the sums.  MxNoLora: none, and no code for it.
 struct MxLora {
-    const float* h;
+    const uint16_t* h;   // [n_tok][blocks][3][16]
     const uint16_t* b;   // [n_adapters][n_out][rank]
     const int32_t* ids;  // [n_tok]
-    int n_adapters, rank, ldh;
+    int n_adapters, rank, blocks;
 };
 struct MxNoLora {};
 
-__device__ __forceinline__ float dot8(u32x4 b, f32x4 h0, f32x4 h1, float s) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        s = fmaf(__uint_as_float(b[i] << 16), i < 2 ? h0[2 * i] : h1[2 * i - 4], s);
-        s = fmaf(__uint_as_float(b[i] & 0xffff0000u), i < 2 ? h0[2 * i + 1] : h1[2 * i - 3], s);
-    }
-    return s;
-}
+__device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // What token t's adapter adds to channels n .. n+3.
 __device__ __forceinline__ f32x4 lora_at(const MxLora& l, int64_t t, int n, int n_out) {
@@ -143,14 +137,24 @@ __device__ __forceinline__ f32x4 lora_at(const MxLora& l, int64_t t, int n, int 
     const int id = l.ids[t];
     if ((unsigned)id >= (unsigned)l.n_adapters) return y;
     const uint16_t* b = l.b + ((int64_t)id * n_out + n) * l.rank;
-    const float* h = l.h + t * l.ldh;
+    const uint16_t* h = l.h + t * l.blocks * 48;
     const int last = n_out - 1 - n;   // rows past the end repeat the last one
 #pragma unroll 2
     for (int r = 0; r < l.rank; r += 8) {
-        const f32x4 h0 = *reinterpret_cast<const f32x4*>(h + r), h1 = *reinterpret_cast<const f32x4*>(h + r + 4);
+        const uint16_t* hr = h + r / 16 * 48 + r % 16;
+        u32x4 p[3], w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            y[j] = dot8(*reinterpret_cast<const u32x4*>(b + min(j, last) * l.rank + r), h0, h1, y[j]);
+        for (int i = 0; i < 3; ++i) p[i] = *reinterpret_cast<const u32x4*>(hr + 16 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const u32x4*>(b + min(j, last) * l.rank + r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // the pieces' sum is exact
+            const float h0 = low_bf16(p[0][i]) + (low_bf16(p[1][i]) + low_bf16(p[2][i]));
+            const float h1 = high_bf16(p[0][i]) + (high_bf16(p[1][i]) + high_bf16(p[2][i]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = fmaf(high_bf16(w[j][i]), h1, fmaf(low_bf16(w[j][i]), h0, y[j]));
+        }
     }
     return y;
 }
@@ -283,6 +287,13 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
 #pragma unroll
     for (int i = 0; i < D; ++i)
         if (s_begin + i < s_end) fetch(s_begin + i, i);
+    // the adapters' share of what this thread puts out, while the first steps arrive
+    static_assert(R * 4 * NC <= kSkinnyThreads, "four channels of a token per thread");
+    f32x4 share = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (std::is_same_v<L, MxLora>) {
+        const int t = threadIdx.x / (4 * NC), c = (threadIdx.x % (4 * NC)) * 4;
+        if (t < toks && n0 + c < p.n_out) share = lora_at(lora, t0 + t, n0 + c, p.n_out);
+    }
 #pragma unroll 1
     for (int st = s_begin; st < s_end; st += D) {
         step(st, 0);
@@ -306,7 +317,7 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
 #pragma unroll
         for (int w = 0; w < kSkinnyWaves; ++w)
             y += *reinterpret_cast<const f32x4*>(&red[(w * R + t) * S::LD + c]);
-        if constexpr (std::is_same_v<L, MxLora>) y += lora_at(lora, t0 + t, n0 + c, p.n_out);
+        if constexpr (std::is_same_v<L, MxLora>) y += share;
         mx_put4<T>(o, t0 + t, n0 + c, y);
     }
 }
@@ -351,55 +362,76 @@ struct TileShape {
     static_assert(WAVES * 16 * kRow <= kScale && kBytes <= 160 * 1024, "fits");
 };
 
-// Adds the adapters' share to the sums of a wave's 16 tokens by 16 NC channels:
-// lane (q, m) holds channels c * 16 + 4q .. of token m.  Sixteen ranks are two
-// MFMAs of 32: the three bf16 pieces of h, which hold its 24 bits, two to the first
-// and one to the second, beside the same rows of B.  One pass per adapter among the
-// 16 tokens; a token takes its own alone, summed apart from the others', so that
-// its result does not depend on theirs.
-template <int NC>
-__device__ __forceinline__ void lora_tile(const MxLora& l, int64_t tok, int64_t n_tok, int n0, int n_out, int n_end,
-                                          f32x4 (&acc)[NC]) {
+// Adds the adapters' share to the sums of a wave's 16 NT tokens by 16 NC channels:
+// lane (q, m) holds channels c * 16 + 4q .. of token m of each 16.  Sixteen ranks are
+// two MFMAs of 32, the first two pieces of h in one and the third in the other, beside
+// the same rows of B.  One pass per adapter among the tokens; a token takes its own
+// alone, summed apart from the others', so that its result does not depend on theirs.
+template <int NT, int NC>
+__device__ __forceinline__ void lora_tile(const MxLora& l, const int (&ids)[NT], int64_t t0, int n0, int n_out,
+                                          int n_end, f32x4 (&acc)[NT][NC]) {
     const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
-    const int id = tok < n_tok ? l.ids[tok] : -1;
-    const bool has = (unsigned)id < (unsigned)l.n_adapters;
-    uint64_t left = __ballot(has);
-    while (left) {
-        const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        const bool mine = has && id == cur;
-        left &= ~__ballot(mine);
-        f32x4 d[NC];
+    uint64_t left[NT];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) d[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const uint16_t* b = l.b + (int64_t)cur * n_out * l.rank;
-#pragma unroll 1
-        for (int r0 = 0; r0 < l.rank; r0 += 16) {
-            const int r = r0 + 8 * (q & 1);
-            bf16x8 h1, h2;
+    for (int t = 0; t < NT; ++t) left[t] = __ballot((unsigned)ids[t] < (unsigned)l.n_adapters);
+    struct Block {
+        u32x4 w[NC], h[NT][2];
+    };
+    while (true) {
+        int cur = -1;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float x = mine ? l.h[tok * l.ldh + r + j] : 0.f;
-                const __bf16 hi = (__bf16)x;
-                const float e = x - (float)hi;
-                // an infinity has no further pieces
-                const __bf16 mid = (__bf16)(fabsf(e) <= 3.0e38f ? e : 0.f);
-                const float f = e - (float)mid;
-                h1[j] = q < 2 ? hi : mid;
-                h2[j] = q < 2 && fabsf(f) <= 3.0e38f ? (__bf16)f : (__bf16)0.f;
-            }
+        for (int t = NT - 1; t >= 0; --t)
+            if (left[t]) cur = __builtin_amdgcn_readlane(ids[t], __builtin_ctzll(left[t]));
+        if (cur < 0) break;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) left[t] &= ~__ballot(ids[t] == cur);
+        const uint16_t* b = l.b + ((int64_t)cur * n_out + n0 + m) * l.rank + 8 * (q & 1);
+        const uint16_t* h = l.h + (t0 + m) * l.blocks * 48 + 8 * q;
+        const u32x4 zero = u32x4{0u, 0u, 0u, 0u};
+        const auto load = [&](int k) {
+            Block x;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                const int n = n0 + c * 16 + m;
-                u32x4 w = u32x4{0u, 0u, 0u, 0u};
-                if (n < n_end && r < l.rank) w = *reinterpret_cast<const u32x4*>(b + (int64_t)n * l.rank + r);
-                d[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), h1, d[c], 0, 0, 0);
-                d[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), h2, d[c], 0, 0, 0);
+                x.w[c] = zero;
+                if (n0 + c * 16 + m < n_end && 16 * k + 8 * (q & 1) < l.rank)
+                    x.w[c] = *reinterpret_cast<const u32x4*>(b + (int64_t)c * 16 * l.rank + 16 * k);
             }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                x.h[t][0] = x.h[t][1] = zero;
+                if (ids[t] == cur) {
+                    const uint16_t* ht = h + ((int64_t)t * 16 * l.blocks + k) * 48;
+                    x.h[t][0] = *reinterpret_cast<const u32x4*>(ht);
+                    if (q < 2) x.h[t][1] = *reinterpret_cast<const u32x4*>(ht + 32);
+                }
+            }
+            return x;
+        };
+        f32x4 d[NT][NC];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) d[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        Block x = load(0);
+        for (int k = 0; k < l.blocks; ++k) {
+            const Block now = x;
+            if (k + 1 < l.blocks) x = load(k + 1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        d[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, now.w[c]),
+                                                                          __builtin_bit_cast(bf16x8, now.h[t][j]),
+                                                                          d[t][c], 0, 0, 0);
         }
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[c][j] = mine ? acc[c][j] + d[c][j] : acc[c][j];
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[t][c][j] = ids[t] == cur ? acc[t][c][j] + d[t][c][j] : acc[t][c][j];
     }
 }
 
@@ -521,6 +553,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut 
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    int ids[NT] = {};
+    if constexpr (std::is_same_v<L, MxLora>) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int64_t tok = t0 + (wt * NT + t) * 16 + m;
+            ids[t] = tok < p.n_tok ? lora.ids[tok] : -1;
+        }
+    }
     constexpr int kVm = 0x0f70, kLgkm0 = 0xc07f;   // wait for all but the low bits' vector loads; for all of LDS
     // the order in which the waits count: what follows a block's tokens
     issue_scales(0);
@@ -597,6 +637,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut 
         if (kb + 1 == blocks) break;
         block(kb + 1, 1);
     }
+    if constexpr (std::is_same_v<L, MxLora>)
+        lora_tile<NT, NC>(lora, ids, t0 + wt * 16 * NT, n0 + wc * 16 * NC, p.n_out, n_end, acc);
     // the loads past the last block are done before their stages are used again
     __builtin_amdgcn_s_waitcnt(0x0070);                          // vmcnt(0) lgkmcnt(0)
     __syncthreads();
@@ -610,8 +652,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut 
     uint8_t* eb = lds + wave * (16 * S::kRow);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        if constexpr (std::is_same_v<L, MxLora>)
-            lora_tile<NC>(lora, tw + t * 16 + m, p.n_tok, nw, p.n_out, n_end, acc[t]);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             *reinterpret_cast<f32x4*>(eb + m * S::kRow + (c * 16 + 4 * q) * 4) = acc[t][c];
@@ -712,7 +752,8 @@ hipError_t launch_any(gdn_dtype out, const MxIn& p, const MxOut& o, const L& lor
 hipError_t launch_with(gdn_dtype out, const MxIn& p, const MxOut& o, const LoraArgs& l, hipStream_t stream) {
     const hipError_t e = launch_lora_shrink(p.n_tok, p.n_in, p.x, p.ld_x, l, stream);
     if (e != hipSuccess) return e;
-    const MxLora lora{l.h, static_cast<const uint16_t*>(l.b), l.ids, l.n_adapters, l.rank, (l.rank + 15) / 16 * 16};
+    const MxLora lora{static_cast<const uint16_t*>(l.h), static_cast<const uint16_t*>(l.b), l.ids,
+                      l.n_adapters, l.rank, (l.rank + 15) / 16};
     return launch_any(out, p, o, lora, stream);
 }
 

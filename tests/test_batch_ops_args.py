@@ -53,7 +53,7 @@ def test_slot_reorder_and_batch_maps_refuse_a_null_pool(lib):
 
 
 LORA = dict(n_tok=2, n_in=64, n_out=10, x=A, ld_x=64, codes=A, scales=A, n=3, rank=16, a=A, b=A, scale=A, ids=A, y_t=1,
-            y=A, ld_y=10, ws=A, ws_bytes=2 * 16 * 4, stream=NUL)
+            y=A, ld_y=10, ws=A, ws_bytes=2 * 96, stream=NUL)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -63,7 +63,7 @@ LORA = dict(n_tok=2, n_in=64, n_out=10, x=A, ld_x=64, codes=A, scales=A, n=3, ra
     ({"a": NUL}, INVALID), ({"b": NUL}, INVALID), ({"scale": NUL}, INVALID), ({"ids": NUL}, INVALID),
     ({"a": A + 8}, INVALID), ({"b": A + 8}, INVALID), ({"scale": A + 2}, INVALID), ({"ids": A + 1}, INVALID),
     ({"x": A + 8}, INVALID), ({"ld_x": 68}, INVALID), ({"ld_y": 9}, INVALID), ({"ws": NUL}, WORKSPACE),
-    ({"ws_bytes": 2 * 16 * 4 - 1}, WORKSPACE), ({"ws": A + 8}, INVALID), ({"rank": 24}, WORKSPACE), ({"n_tok": 0}, OK),
+    ({"ws_bytes": 2 * 96 - 1}, WORKSPACE), ({"ws": A + 8}, INVALID), ({"rank": 24}, WORKSPACE), ({"n_tok": 0}, OK),
     ({"n_tok": 0, "n": 0, "rank": 3}, OK),
 ])
 def test_mx_proj_lora_refusals(lib, change, status):
@@ -74,7 +74,7 @@ def test_mx_lora_workspaces(lib):
     n = ctypes.c_size_t(7)
     assert lib.gdn_mx_proj_lora_workspace_bytes(4, 64, 8, 12, ctypes.byref(n)) == UNSUPPORTED and n.value == 7
     assert lib.gdn_mx_proj_lora_workspace_bytes(4, 64, 8, 16, NUL) == INVALID
-    assert lib.gdn_mx_proj_lora_workspace_bytes(4, 64, 8, 24, ctypes.byref(n)) == OK and n.value == 4 * 32 * 4
+    assert lib.gdn_mx_proj_lora_workspace_bytes(4, 64, 8, 24, ctypes.byref(n)) == OK and n.value == 4 * 2 * 96
     assert lib.gdn_mx_in_proj_lora_workspace_bytes(NUL, 4, 64, 16, 1, ctypes.byref(n)) == INVALID
     assert lib.gdn_mx_in_proj_lora(NUL, 1, 64, A, A, A, 1, 16, *([A] * 10), A, 64, NUL) == INVALID
 
