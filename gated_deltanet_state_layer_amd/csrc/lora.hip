@@ -8,12 +8,11 @@
 #include <algorithm>
 
 #include "gdn_common.h"
+#include "lds_load.h"
 #include "mfma_split.h"
 
 namespace gdn {
 namespace {
-
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float s) {
 #pragma unroll
@@ -58,59 +57,109 @@ __global__ __launch_bounds__(kThreads) void lora_rows_kernel(LoraArgs l, const u
     if (lane == 0) put_pieces(static_cast<uint16_t*>(l.h), t, blocks, r, l.scale[id] * s);
 }
 
-// Many tokens: 16 of them to a workgroup, the input axis split over its eight waves,
-// on the matrix cores (A's rows times the tokens), the partial sums added in LDS.
-// One pass per adapter among the 16 tokens; each token keeps its own.
-constexpr int kTileWaves = 8, kTileThreads = kTileWaves * 64;
+// Many tokens: 16 of them by 16 RB ranks to a workgroup, on the matrix cores (A's rows
+// times the tokens), the partial sums of its four waves added in LDS.  A wave takes
+// every fourth 128 inputs, two steps of them through LDS of its own (no barrier) by
+// loads that store straight into it: they read rows in pieces of 256 bytes from
+// neighbouring lanes, where loads in the matrix operands' layout take 64 bytes each.
+// One pass per adapter among the 16 tokens, each token keeping its own; of several
+// passes workgroup z takes every gridDim.z-th.
+constexpr int kTileWaves = 4, kTileThreads = kTileWaves * 64;
 
 template <int RB>
 __global__ __launch_bounds__(kTileThreads) void lora_tile_kernel(LoraArgs l, const uint16_t* x, int64_t ld_x,
-                                                                int64_t n_tok, int n_in, int blocks, int r0) {
-    __shared__ __align__(16) float part[kTileWaves][16][16 * RB + 4];   // [wave][token][rank]
+                                                                int64_t n_tok, int n_in, int blocks) {
+    constexpr int kRows = 16 * (1 + RB), kStage = kRows * 256, kLoads = kRows / 4, LD = 16 * RB + 4;
+    extern __shared__ __align__(16) uint8_t lds[];   // [wave][2 steps][16 tokens, 16 RB rows of A][256]
     const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t0 = (int64_t)blockIdx.x * 16, t = min(t0 + m, n_tok - 1);
-    const int id = t0 + m < n_tok ? l.ids[t] : -1;
+    const int64_t t0 = (int64_t)blockIdx.x * 16;
+    const int toks = (int)min((int64_t)16, n_tok - t0), r0 = blockIdx.y * (16 * RB), rows = min(16 * RB, l.rank - r0);
+    const int id = m < toks ? l.ids[t0 + m] : -1;
     const bool has = (unsigned)id < (unsigned)l.n_adapters;
-    const int steps = n_in / 32, per = (steps + kTileWaves - 1) / kTileWaves;
-    const int begin = wave * per, end = min(steps, begin + per);
-    const uint16_t* xt = x + t * ld_x + 8 * q;
-    uint64_t left = __ballot(has);
-    while (left) {
-        const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        const bool mine = has && id == cur;
-        left &= ~__ballot(mine);
-        const uint16_t* a[RB];   // rows past the rank repeat the last one; what they give is dropped
+    const int steps = (n_in + 127) / 128;
+    const auto x_rs = buf_rsrc(x + t0 * ld_x, ((toks - 1) * ld_x + n_in) * 2);
+    uint8_t* mine = lds + wave * (2 * kStage);
+    // Slot s of a row's 16 holds chunk s ^ row % 16, so the 16 rows of a fragment read
+    // spread over all banks.
+    int chunk[4], at[kLoads];
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
-            a[b] = static_cast<const uint16_t*>(l.a) +
-                   ((int64_t)cur * l.rank + min(r0 + 16 * b + m, l.rank - 1)) * n_in + 8 * q;
+    for (int i = 0; i < kLoads; ++i) {
+        const int r = i * 4 + q;
+        if (i < 4) chunk[i] = m ^ (r & 15);
+        at[i] = i < 4 ? offset_if(r < toks, (int)(r * ld_x) * 2 + chunk[i] * 16)
+                      : offset_if(r - 16 < rows, (r - 16) * n_in * 2 + chunk[i & 3] * 16);
+    }
+    uint64_t left = __ballot(has);
+    for (unsigned pass = 0; left; ++pass) {
+        const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        const uint64_t tokens = __ballot(has && id == cur);
+        left &= ~tokens;
+        if (pass % gridDim.z != blockIdx.z) continue;
+        const auto a_rs = buf_rsrc(static_cast<const uint16_t*>(l.a) + ((int64_t)cur * l.rank + r0) * n_in,
+                                   (int64_t)rows * n_in * 2);
+        const auto fetch = [&](int s, int b) {   // past the row's end zeros
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                load_lds16(i < 4 ? x_rs : a_rs, mine + b * kStage + i * 1024,
+                           offset_if(s * 128 + chunk[i & 3] * 8 < n_in, at[i]), s * 256);
+        };
         f32x4 acc[RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int s = begin; s < end; ++s) {
-            const bf16x8 xv = *reinterpret_cast<const bf16x8*>(xt + s * 32);
+        if (wave < steps) fetch(wave, 0);
+        if (wave + kTileWaves < steps) fetch(wave + kTileWaves, 1);
+        for (int s = wave, b = 0; s < steps; s += kTileWaves, b ^= 1) {
+            // this step's loads have arrived, the next one's may be on their way
+            if (s + kTileWaves < steps) __builtin_amdgcn_s_waitcnt(0x0f70 | kLoads);
+            else __builtin_amdgcn_s_waitcnt(0x0f70);
+            __builtin_amdgcn_sched_barrier(0);
+            const uint8_t* base = mine + b * kStage + m * 256;
 #pragma unroll
-            for (int b = 0; b < RB; ++b)
-                acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const bf16x8*>(a[b] + s * 32), xv,
-                                                                 acc[b], 0, 0, 0);
+            for (int j = 0; j < 4; ++j) {
+                const int slot = ((q * 4 + j) ^ m) * 16;
+                const bf16x8 xv = *reinterpret_cast<const bf16x8*>(base + slot);
+#pragma unroll
+                for (int c = 0; c < RB; ++c)
+                    acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        *reinterpret_cast<const bf16x8*>(base + (1 + c) * 4096 + slot), xv, acc[c], 0, 0, 0);
+            }
+            __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the stage is read
+            __builtin_amdgcn_sched_barrier(0);
+            if (s + 2 * kTileWaves < steps) fetch(s + 2 * kTileWaves, b);
         }
+        __syncthreads();   // every wave is done with its stages
+        float* part = reinterpret_cast<float*>(lds);   // [wave][token][LD]
 #pragma unroll
-        for (int b = 0; b < RB; ++b) *reinterpret_cast<f32x4*>(&part[wave][m][16 * b + 4 * q]) = acc[b];
+        for (int c = 0; c < RB; ++c)
+            *reinterpret_cast<f32x4*>(&part[(wave * 16 + m) * LD + 16 * c + 4 * q]) = acc[c];
         __syncthreads();
-        const float scale = l.scale[cur];
-        for (int i = threadIdx.x; i < 16 * 16 * RB; i += kTileThreads) {
-            const int tok = i / (16 * RB), r = i % (16 * RB);
-            if (__shfl(mine ? 1 : 0, tok) == 0) continue;
+#pragma unroll
+        for (int c = 0; c < RB; ++c) {
+            const int tok = threadIdx.x / 16, r = 16 * c + threadIdx.x % 16;
+            if (!(tokens >> tok & 1) || r0 + r >= 16 * blocks) continue;
             float sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < kTileWaves; ++w) sum += part[w][tok][r];
-            if (r0 + r < 16 * blocks)
-                put_pieces(static_cast<uint16_t*>(l.h), t0 + tok, blocks, r0 + r, r0 + r < l.rank ? scale * sum : 0.f);
+            for (int w = 0; w < kTileWaves; ++w) sum += part[(w * 16 + tok) * LD + r];
+            put_pieces(static_cast<uint16_t*>(l.h), t0 + tok, blocks, r0 + r, r < rows ? l.scale[cur] * sum : 0.f);
         }
         __syncthreads();
     }
+}
+
+template <int RB>
+hipError_t tiles(int64_t n_tok, int32_t n_in, const uint16_t* x, int64_t ld_x, const LoraArgs& l, hipStream_t stream) {
+    constexpr int lds = kTileWaves * 2 * 16 * (1 + RB) * 256;
+    static std::atomic<uint64_t> done{0};
+    if (lds > 65536) {
+        const hipError_t e = allow_dynamic_lds(&lora_tile_kernel<RB>, lds, &done);
+        if (e != hipSuccess) return e;
+    }
+    const int blocks = (l.rank + 15) / 16, y = (blocks + RB - 1) / RB;
+    const int64_t n = (n_tok + 15) / 16, z = std::min<int64_t>(16, std::max<int64_t>(1, 256 / (n * y)));
+    hipLaunchKernelGGL(lora_tile_kernel<RB>, dim3((unsigned)n, y, (unsigned)z), dim3(kTileThreads), lds, stream, l, x,
+                       ld_x, n_tok, n_in, blocks);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -121,25 +170,12 @@ hipError_t launch_lora_shrink(int64_t n_tok, int32_t n_in, const void* x, int64_
                               hipStream_t stream) {
     const int blocks = (l.rank + 15) / 16;
     const uint16_t* xp = static_cast<const uint16_t*>(x);
-    if (n_tok <= 128) {
+    if (n_tok * blocks <= 768) {
         hipLaunchKernelGGL(lora_rows_kernel, dim3((unsigned)(n_tok * blocks * 16 / kWaves)), dim3(kThreads), 0, stream,
                            l, xp, ld_x, n_in, blocks);
         return hipGetLastError();
     }
-    const dim3 grid((unsigned)((n_tok + 15) / 16));
-    for (int b = 0; b < blocks;) {
-        const int r0 = 16 * b, more = blocks - b;
-        if (more >= 2) {
-            hipLaunchKernelGGL(lora_tile_kernel<2>, grid, dim3(kTileThreads), 0, stream, l, xp, ld_x, n_tok, n_in,
-                               blocks, r0);
-            b += 2;
-        } else {
-            hipLaunchKernelGGL(lora_tile_kernel<1>, grid, dim3(kTileThreads), 0, stream, l, xp, ld_x, n_tok, n_in,
-                               blocks, r0);
-            b += 1;
-        }
-    }
-    return hipGetLastError();
+    return blocks == 1 ? tiles<1>(n_tok, n_in, xp, ld_x, l, stream) : tiles<2>(n_tok, n_in, xp, ld_x, l, stream);
 }
 
 }  // namespace gdn

@@ -13,28 +13,12 @@
 #include <type_traits>
 
 #include "gdn_common.h"
+#include "lds_load.h"
 #include "mfma_split.h"
 #include "mx_plan.h"
 
 namespace gdn {
 namespace {
-
-constexpr int kRsrcWord3 = 0x00020000;
-constexpr int kOffOOB = 0x7ffffff0;   // past every descriptor: loads return zeros
-
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-using lds_ptr = __attribute__((address_space(3))) void*;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void* p, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, kRsrcWord3);
-}
-
-// 16 bytes per lane from base + offset + soffset straight into LDS, lane l's at
-// dst + 16 l.
-__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rs, void* dst, int offset, int soffset) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)dst, 16, offset, soffset, 0, 0);
-}
 
 // Where the output channels go: [0, end[0]) to seg[0], [end[0], end[1]) to
 // seg[1], and so on, ld elements between tokens; from end[3] on, fp32 gates a
@@ -109,14 +93,6 @@ __device__ __forceinline__ bf16x8 mx_expand(uint32_t c, float scale) {
     return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
 
-// An offset, or one past every descriptor.  Opaque to the compiler, which would
-// otherwise split the load into two branches with a wait between them.
-__device__ __forceinline__ int offset_if(bool in, int offset) {
-    int v = in ? offset : kOffOOB;
-    asm("" : "+v"(v));
-    return v;
-}
-
 // A low-rank adapter per token beside the weights: token t's h[t] (scale x A^T of
 // its adapter, in three bf16 pieces by blocks of 16 ranks: see lora.hip) times the
 // rows of its adapter's B is added to the sums.  MxNoLora: none, and no code for it.
@@ -126,37 +102,46 @@ struct MxLora {
     const int32_t* ids;  // [n_tok]
     int n_adapters, rank, blocks;
 };
-struct MxNoLora {};
+struct MxNoLora {
+    MxNoLora() = default;
+    __device__ __forceinline__ MxNoLora(const MxNoLora&, int64_t, int) {}
+};
+constexpr int kLoraAhead = 64;   // ranks whose rows of B have LDS of their own in the tile kernel
+__device__ __forceinline__ int lora_ranks(const MxLora& l) { return l.rank; }
+__device__ __forceinline__ int lora_ranks(const MxNoLora&) { return 0; }
 
 __device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// What token t's adapter adds to channels n .. n+3.
-__device__ __forceinline__ f32x4 lora_at(const MxLora& l, int64_t t, int n, int n_out) {
-    f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
+// A thread's part of what token t's adapter adds to channels n0 .. of a tile: thread
+// j of the token's takes rank 8 (j % 2) .. of each 16 and channels step i + j / 2, so
+// that neighbouring lanes read B side by side.
+__device__ __forceinline__ void lora_share(const MxLora& l, int64_t t, int n0, int n_out, int j, int step,
+                                           float (&y)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = 0.f;
     const int id = l.ids[t];
-    if ((unsigned)id >= (unsigned)l.n_adapters) return y;
-    const uint16_t* b = l.b + ((int64_t)id * n_out + n) * l.rank;
-    const uint16_t* h = l.h + t * l.blocks * 48;
-    const int last = n_out - 1 - n;   // rows past the end repeat the last one
-#pragma unroll 2
-    for (int r = 0; r < l.rank; r += 8) {
-        const uint16_t* hr = h + r / 16 * 48 + r % 16;
-        u32x4 p[3], w[4];
+    if ((unsigned)id >= (unsigned)l.n_adapters) return;
+    const int r0 = 8 * (j & 1);
+    const uint16_t* b = l.b + ((int64_t)id * n_out + n0) * l.rank + r0;
+    const uint16_t* h = l.h + t * l.blocks * 48 + r0;
+    const int last = n_out - 1 - n0;   // rows past the end repeat the last one
+#pragma unroll 1
+    for (int r = 0; r + r0 < l.rank; r += 16, h += 48) {
+        u32x4 p[3], w[8];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) p[i] = *reinterpret_cast<const u32x4*>(hr + 16 * i);
+        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const u32x4*>(b + min(i * step + j / 2, last) * l.rank + r);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const u32x4*>(b + min(j, last) * l.rank + r);
+        for (int i = 0; i < 3; ++i) p[i] = *reinterpret_cast<const u32x4*>(h + 16 * i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int k = 0; k < 4; ++k) {
             // the pieces' sum is exact
-            const float h0 = low_bf16(p[0][i]) + (low_bf16(p[1][i]) + low_bf16(p[2][i]));
-            const float h1 = high_bf16(p[0][i]) + (high_bf16(p[1][i]) + high_bf16(p[2][i]));
+            const float h0 = low_bf16(p[0][k]) + (low_bf16(p[1][k]) + low_bf16(p[2][k]));
+            const float h1 = high_bf16(p[0][k]) + (high_bf16(p[1][k]) + high_bf16(p[2][k]));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = fmaf(high_bf16(w[j][i]), h1, fmaf(low_bf16(w[j][i]), h0, y[j]));
+            for (int i = 0; i < 8; ++i) y[i] = fmaf(high_bf16(w[i][k]), h1, fmaf(low_bf16(w[i][k]), h0, y[i]));
         }
     }
-    return y;
 }
 
 struct MxIn {
@@ -192,6 +177,7 @@ struct SkinnyShape {
     static constexpr int LD = 16 * NC + 4;
     static constexpr int kLoads = kSkinnyWaves * D * kStage, kSums = kSkinnyWaves * R * LD * 4;
     static constexpr int kBytes = kLoads > kSums ? kLoads : kSums;
+    static constexpr int kLoraSums = kSums + R * LD * 4, kLoraBytes = kLoads > kLoraSums ? kLoads : kLoraSums;
     static constexpr int kAhead = (D - 1) * (1 + NC + XL);   // loads of the steps behind the present one
     static_assert((R == 4 || R % 16 == 0) && NC <= 4 && D <= 2 && kAhead < 64, "the schedule");
 };
@@ -287,12 +273,13 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
 #pragma unroll
     for (int i = 0; i < D; ++i)
         if (s_begin + i < s_end) fetch(s_begin + i, i);
-    // the adapters' share of what this thread puts out, while the first steps arrive
-    static_assert(R * 4 * NC <= kSkinnyThreads, "four channels of a token per thread");
-    f32x4 share = f32x4{0.f, 0.f, 0.f, 0.f};
+    // The adapters' share, while the first steps arrive: 4 NC threads to a token, each
+    // with half the ranks of eight channels.
+    float share[8];
+    const int st_tok = threadIdx.x / (4 * NC), st_j = threadIdx.x % (4 * NC);
     if constexpr (std::is_same_v<L, MxLora>) {
-        const int t = threadIdx.x / (4 * NC), c = (threadIdx.x % (4 * NC)) * 4;
-        if (t < toks && n0 + c < p.n_out) share = lora_at(lora, t0 + t, n0 + c, p.n_out);
+        static_assert(R * 4 * NC <= kSkinnyThreads, "every token has its threads");
+        if (st_tok < toks) lora_share(lora, t0 + st_tok, n0, p.n_out, st_j, 2 * NC, share);
     }
 #pragma unroll 1
     for (int st = s_begin; st < s_end; st += D) {
@@ -308,6 +295,14 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
 #pragma unroll
             for (int c = 0; c < NC; ++c)
                 *reinterpret_cast<f32x4*>(&red[(wave * R + t * 16 + m) * S::LD + c * 16 + 4 * q]) = acc[t][c];
+    constexpr bool kLora = std::is_same_v<L, MxLora>;
+    if constexpr (kLora)
+        if (st_tok < toks)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float both = group_sum<2>(share[i]);
+                if (!(st_j & 1)) red[(kSkinnyWaves * R + st_tok) * S::LD + i * 2 * NC + st_j / 2] = both;
+            }
     __syncthreads();
 #pragma unroll 1
     for (int i = threadIdx.x; i < R * 4 * NC; i += kSkinnyThreads) {
@@ -315,9 +310,8 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
         if (t >= toks || n0 + c >= p.n_out) continue;
         f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kSkinnyWaves; ++w)
+        for (int w = 0; w < kSkinnyWaves + (kLora ? 1 : 0); ++w)
             y += *reinterpret_cast<const f32x4*>(&red[(w * R + t) * S::LD + c]);
-        if constexpr (std::is_same_v<L, MxLora>) y += share;
         mx_put4<T>(o, t0 + t, n0 + c, y);
     }
 }
@@ -362,83 +356,107 @@ struct TileShape {
     static_assert(WAVES * 16 * kRow <= kScale && kBytes <= 160 * 1024, "fits");
 };
 
-// Adds the adapters' share to the sums of a wave's 16 NT tokens by 16 NC channels:
+// The adapters among a tile's tokens, one after the other.  Every wave holds all the
+// tile's ids, two to a lane, and so comes to the same order by itself.
+struct LoraOrder {
+    int id[2];
+    uint64_t left[2];
+    __device__ __forceinline__ LoraOrder(const MxLora& l, int64_t t0, int toks) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) id[i] = i * 64 + lane < toks ? l.ids[t0 + i * 64 + lane] : -1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) left[i] = __ballot((unsigned)id[i] < (unsigned)l.n_adapters);
+    }
+    // The next adapter, -1 behind the last.
+    __device__ __forceinline__ int next() {
+        if (!(left[0] | left[1])) return -1;
+        const int cur = left[0] ? __builtin_amdgcn_readlane(id[0], __builtin_ctzll(left[0]))
+                                : __builtin_amdgcn_readlane(id[1], __builtin_ctzll(left[1]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) left[i] &= ~__ballot(id[i] == cur);
+        return cur;
+    }
+};
+
+// An adapter's rows of B for a tile's channels into LDS, as they lie; zeros past the
+// last row.
+__device__ __forceinline__ void lora_stage(const MxLora& l, int cur, int n0, int n_out, int rows, int channels,
+                                           uint8_t* dst) {
+    const auto rs = buf_rsrc(l.b + ((int64_t)cur * n_out + n0) * l.rank, (int64_t)rows * l.rank * 2);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int loads = channels * l.rank / 512;   // of 1 KiB; channels are a multiple of 64
+    for (int i = wave; i < loads; i += kMxWorkgroup / 64) load_lds16(rs, dst + i * 1024, i * 1024 + lane * 16, 0);
+}
+
+// The pieces of h of a wave's tokens for 16 ranks, the first two pieces as one operand
+// and the third as another.  Tokens without an adapter bring what lies there.
+template <int NT>
+struct LoraPieces {
+    u32x4 v[NT][2];
+    __device__ __forceinline__ void load(const MxLora& l, int64_t t0, int64_t n_tok, int k) {
+        const int m = threadIdx.x & 15, q = threadIdx.x >> 4 & 3;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const uint16_t* h = l.h + (min(t0 + t * 16 + m, n_tok - 1) * l.blocks + k) * 48;
+            v[t][0] = *reinterpret_cast<const u32x4*>(h + 8 * q);
+            const u32x4 third = *reinterpret_cast<const u32x4*>(h + 32 + 8 * (q & 1));
+            v[t][1] = q < 2 ? third : u32x4{0u, 0u, 0u, 0u};
+        }
+    }
+};
+
+// Adds adapter cur's share to the sums of a wave's 16 NT tokens by 16 NC channels:
 // lane (q, m) holds channels c * 16 + 4q .. of token m of each 16.  Sixteen ranks are
-// two MFMAs of 32, the first two pieces of h in one and the third in the other, beside
-// the same rows of B.  One pass per adapter among the tokens; a token takes its own
-// alone, summed apart from the others', so that its result does not depend on theirs.
+// two MFMAs of 32 beside the same rows of B.  A token takes its own adapter's alone,
+// summed apart from the others', so that its result does not depend on theirs.
 template <int NT, int NC>
-__device__ __forceinline__ void lora_tile(const MxLora& l, const int (&ids)[NT], int64_t t0, int n0, int n_out,
-                                          int n_end, f32x4 (&acc)[NT][NC]) {
+__device__ __forceinline__ void lora_add(const MxLora& l, int cur, const int (&ids)[NT], int64_t t0, int64_t n_tok,
+                                         const LoraPieces<NT>& first, const uint8_t* b, f32x4 (&acc)[NT][NC]) {
     const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
-    uint64_t left[NT];
+    bool any = false;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) left[t] = __ballot((unsigned)ids[t] < (unsigned)l.n_adapters);
-    struct Block {
-        u32x4 w[NC], h[NT][2];
-    };
-    while (true) {
-        int cur = -1;
+    for (int t = 0; t < NT; ++t) any |= __any(ids[t] == cur);
+    if (!any) return;
+    f32x4 d[NT][NC];
 #pragma unroll
-        for (int t = NT - 1; t >= 0; --t)
-            if (left[t]) cur = __builtin_amdgcn_readlane(ids[t], __builtin_ctzll(left[t]));
-        if (cur < 0) break;
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) left[t] &= ~__ballot(ids[t] == cur);
-        const uint16_t* b = l.b + ((int64_t)cur * n_out + n0 + m) * l.rank + 8 * (q & 1);
-        const uint16_t* h = l.h + (t0 + m) * l.blocks * 48 + 8 * q;
-        const u32x4 zero = u32x4{0u, 0u, 0u, 0u};
-        const auto load = [&](int k) {
-            Block x;
+        for (int c = 0; c < NC; ++c) d[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    LoraPieces<NT> h = first;
+    for (int k = 0; k < l.blocks; ++k) {
+        const LoraPieces<NT> now = h;
+        if (k + 1 < l.blocks) h.load(l, t0, n_tok, k + 1);
+        const bool in = 16 * k + 8 * (q & 1) < l.rank;
+        u32x4 w[NC];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                x.w[c] = zero;
-                if (n0 + c * 16 + m < n_end && 16 * k + 8 * (q & 1) < l.rank)
-                    x.w[c] = *reinterpret_cast<const u32x4*>(b + (int64_t)c * 16 * l.rank + 16 * k);
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                x.h[t][0] = x.h[t][1] = zero;
-                if (ids[t] == cur) {
-                    const uint16_t* ht = h + ((int64_t)t * 16 * l.blocks + k) * 48;
-                    x.h[t][0] = *reinterpret_cast<const u32x4*>(ht);
-                    if (q < 2) x.h[t][1] = *reinterpret_cast<const u32x4*>(ht + 32);
-                }
-            }
-            return x;
-        };
-        f32x4 d[NT][NC];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int c = 0; c < NC; ++c) d[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-        Block x = load(0);
-        for (int k = 0; k < l.blocks; ++k) {
-            const Block now = x;
-            if (k + 1 < l.blocks) x = load(k + 1);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        d[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, now.w[c]),
-                                                                          __builtin_bit_cast(bf16x8, now.h[t][j]),
-                                                                          d[t][c], 0, 0, 0);
+        for (int c = 0; c < NC; ++c) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(b + (c * 16 + m) * l.rank * 2 + (in ? 32 * k + 16 * (q & 1) : 0));
+            w[c] = in ? v : u32x4{0u, 0u, 0u, 0u};
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[t][c][j] = ids[t] == cur ? acc[t][c][j] + d[t][c][j] : acc[t][c][j];
+                for (int c = 0; c < NC; ++c)
+                    d[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[c]),
+                                                                      __builtin_bit_cast(bf16x8, now.v[t][j]), d[t][c],
+                                                                      0, 0, 0);
     }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t][c][j] = ids[t] == cur ? acc[t][c][j] + d[t][c][j] : acc[t][c][j];
 }
 
 template <typename T, int NC, typename L>
 __global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut o, int tiles_t, int n_end, L lora) {
     using S = TileShape<NC>;
     constexpr int NT = S::NT;
+    constexpr bool kLora = std::is_same_v<L, MxLora>;
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -460,6 +478,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut 
     const int half = p.n_in / 2, groups = p.n_in / 32, blocks = (groups + 1) / 2, pairs = (groups + 3) / 4;
     const auto x_rs = buf_rsrc(p.x + t0 * p.ld_x, ((toks - 1) * p.ld_x + p.n_in) * 2);
     const auto w_rs = buf_rsrc(p.codes + (int64_t)n0 * half, (int64_t)rows * half);
+    [[maybe_unused]] std::conditional_t<kLora, LoraOrder, MxNoLora> order(lora, t0, toks);
+    [[maybe_unused]] std::conditional_t<kLora, LoraPieces<NT>, MxNoLora> pieces;
 
     // Loads into LDS: lane l of a wave's load writes 16 bytes at 16 l, i.e.
     // eight rows of tokens or 16 rows of weights.  Slot s of a token row holds
@@ -553,14 +573,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut 
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    int ids[NT] = {};
-    if constexpr (std::is_same_v<L, MxLora>) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int64_t tok = t0 + (wt * NT + t) * 16 + m;
-            ids[t] = tok < p.n_tok ? lora.ids[tok] : -1;
-        }
-    }
     constexpr int kVm = 0x0f70, kLgkm0 = 0xc07f;   // wait for all but the low bits' vector loads; for all of LDS
     // the order in which the waits count: what follows a block's tokens
     issue_scales(0);
@@ -574,6 +586,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut 
     issue_x(2, 2);
     issue_x(3, 3);
     __builtin_amdgcn_sched_barrier(0);
+    // Ranks up to kLoraAhead: the first adapter's rows arrive beside the first blocks.
+    // The waits that count loads then wait for these as well.
+    [[maybe_unused]] int lora_cur = -1;
+    [[maybe_unused]] const bool ahead = lora_ranks(lora) <= kLoraAhead;
+    if constexpr (kLora) {
+        lora_cur = order.next();
+        if (ahead && lora_cur >= 0) lora_stage(lora, lora_cur, n0, p.n_out, rows, S::CC, lds + S::kBytes);
+        pieces.load(lora, t0 + wt * 16 * NT, p.n_tok, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    }
     __builtin_amdgcn_s_waitcnt(kVm | (S::WL + 3 * S::XL));
     put_scales(0);
     __builtin_amdgcn_s_waitcnt(kLgkm0);
@@ -637,11 +659,36 @@ __global__ __launch_bounds__(kTileThreads, 2) void mx_tile_kernel(MxIn p, MxOut 
         if (kb + 1 == blocks) break;
         block(kb + 1, 1);
     }
-    if constexpr (std::is_same_v<L, MxLora>)
-        lora_tile<NT, NC>(lora, ids, t0 + wt * 16 * NT, n0 + wc * 16 * NC, p.n_out, n_end, acc);
     // the loads past the last block are done before their stages are used again
     __builtin_amdgcn_s_waitcnt(0x0070);                          // vmcnt(0) lgkmcnt(0)
     __syncthreads();
+
+    // The adapters' share, the next one's rows of B on their way meanwhile.
+    if constexpr (kLora) {
+        int ids[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = (wt * NT + t) * 16 + m;
+            ids[t] = __shfl(order.id[r >= 64], r & 63);
+        }
+        constexpr int kHalf = S::CC * GDN_LORA_MAX_RANK * 2;
+        static_assert(2 * kHalf <= S::kScale, "two adapters' rows in the stages");
+        const auto place = [&](int i) { return lds + (i == 0 && ahead ? S::kBytes : (i & 1) * kHalf); };
+        if (!ahead && lora_cur >= 0) {
+            lora_stage(lora, lora_cur, n0, p.n_out, rows, S::CC, place(0));
+            __builtin_amdgcn_s_waitcnt(0x0f70);                  // vmcnt(0)
+            __syncthreads();
+        }
+        for (int i = 0; lora_cur >= 0; ++i) {
+            const int then = order.next();
+            if (then >= 0) lora_stage(lora, then, n0, p.n_out, rows, S::CC, place(i + 1));
+            lora_add<NT, NC>(lora, lora_cur, ids, t0 + wt * 16 * NT, p.n_tok, pieces, place(i) + wc * 16 * NC * lora.rank * 2,
+                             acc);
+            __builtin_amdgcn_s_waitcnt(0x0f70);                  // vmcnt(0): the next rows are there
+            __syncthreads();
+            lora_cur = then;
+        }
+    }
 
     // 16 tokens at a time through LDS, each wave its own rows, so that a token's
     // channels leave in 16-byte pieces side by side
@@ -696,7 +743,7 @@ bool fits(const void* p, int64_t ld, int elem, int vec) {
 
 template <typename T, int R, int NC, int D = 2, typename L>
 hipError_t skinny(const MxIn& p, const MxOut& o, const MxLaunch& l, const L& lora, hipStream_t stream) {
-    constexpr int lds = SkinnyShape<R, NC, D>::kBytes;
+    constexpr int lds = std::is_same_v<L, MxLora> ? SkinnyShape<R, NC, D>::kLoraBytes : SkinnyShape<R, NC, D>::kBytes;
     static_assert(lds <= 160 * 1024, "fits");
     if (lds > 65536) {
         static std::atomic<uint64_t> done{0};
@@ -712,10 +759,12 @@ hipError_t skinny(const MxIn& p, const MxOut& o, const MxLaunch& l, const L& lor
 template <typename T, int NC, typename L>
 hipError_t tile(const MxIn& p, const MxOut& o, const MxLaunch& l, const L& lora, hipStream_t stream) {
     using S = TileShape<NC>;
+    constexpr int lds = S::kBytes + (std::is_same_v<L, MxLora> ? S::CC * kLoraAhead * 2 : 0);
+    static_assert(lds <= 160 * 1024, "fits");
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_dynamic_lds(&mx_tile_kernel<T, NC, L>, S::kBytes, &done);
+    const hipError_t e = allow_dynamic_lds(&mx_tile_kernel<T, NC, L>, lds, &done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((mx_tile_kernel<T, NC, L>), dim3((unsigned)l.workgroups), dim3(kTileThreads), S::kBytes, stream,
+    hipLaunchKernelGGL((mx_tile_kernel<T, NC, L>), dim3((unsigned)l.workgroups), dim3(kTileThreads), lds, stream,
                        p, o, (int)((p.n_tok + kTileTokens - 1) / kTileTokens), l.c1, lora);
     return hipGetLastError();
 }
