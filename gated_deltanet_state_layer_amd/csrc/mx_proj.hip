@@ -113,24 +113,22 @@ __device__ __forceinline__ int lora_ranks(const MxNoLora&) { return 0; }
 __device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// A thread's part of what token t's adapter adds to channels n0 .. of a tile: thread
-// j of the token's takes rank 8 (j % 2) .. of each 16 and channels step i + j / 2, so
-// that neighbouring lanes read B side by side.
-__device__ __forceinline__ void lora_share(const MxLora& l, int64_t t, int n0, int n_out, int j, int step,
-                                           float (&y)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = 0.f;
+// A thread's part of what token t's adapter adds to a tile's 16 NC channels: thread j
+// of the token's TPT takes half the ranks of each 16, and channels i TPT / 2 + j / 2,
+// so that neighbouring lanes read B side by side.
+template <int TPT, int E>
+__device__ __forceinline__ void lora_share(const MxLora& l, int64_t t, int n0, int n_out, int j, float (&y)[E]) {
     const int id = l.ids[t];
     if ((unsigned)id >= (unsigned)l.n_adapters) return;
-    const int r0 = 8 * (j & 1);
+    const int r0 = 8 * (j & 1), last = n_out - 1 - n0;   // rows past the end repeat the last one
     const uint16_t* b = l.b + ((int64_t)id * n_out + n0) * l.rank + r0;
     const uint16_t* h = l.h + t * l.blocks * 48 + r0;
-    const int last = n_out - 1 - n0;   // rows past the end repeat the last one
 #pragma unroll 1
     for (int r = 0; r + r0 < l.rank; r += 16, h += 48) {
-        u32x4 p[3], w[8];
+        u32x4 w[E], p[3];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const u32x4*>(b + min(i * step + j / 2, last) * l.rank + r);
+        for (int i = 0; i < E; ++i)
+            w[i] = *reinterpret_cast<const u32x4*>(b + min(i * (TPT / 2) + j / 2, last) * l.rank + r);
 #pragma unroll
         for (int i = 0; i < 3; ++i) p[i] = *reinterpret_cast<const u32x4*>(h + 16 * i);
 #pragma unroll
@@ -139,7 +137,7 @@ __device__ __forceinline__ void lora_share(const MxLora& l, int64_t t, int n0, i
             const float h0 = low_bf16(p[0][k]) + (low_bf16(p[1][k]) + low_bf16(p[2][k]));
             const float h1 = high_bf16(p[0][k]) + (high_bf16(p[1][k]) + high_bf16(p[2][k]));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmaf(high_bf16(w[i][k]), h1, fmaf(low_bf16(w[i][k]), h0, y[i]));
+            for (int i = 0; i < E; ++i) y[i] = fmaf(high_bf16(w[i][k]), h1, fmaf(low_bf16(w[i][k]), h0, y[i]));
         }
     }
 }
@@ -273,14 +271,14 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
 #pragma unroll
     for (int i = 0; i < D; ++i)
         if (s_begin + i < s_end) fetch(s_begin + i, i);
-    // The adapters' share, while the first steps arrive: 4 NC threads to a token, each
-    // with half the ranks of eight channels.
-    float share[8];
-    const int st_tok = threadIdx.x / (4 * NC), st_j = threadIdx.x % (4 * NC);
-    if constexpr (std::is_same_v<L, MxLora>) {
-        static_assert(R * 4 * NC <= kSkinnyThreads, "every token has its threads");
-        if (st_tok < toks) lora_share(lora, t0 + st_tok, n0, p.n_out, st_j, 2 * NC, share);
-    }
+    // The adapters' share, while the first steps arrive: every thread has a token.
+    constexpr bool kLora = std::is_same_v<L, MxLora>;
+    constexpr int kPerToken = kSkinnyThreads / R, kShare = (32 * NC + kPerToken - 1) / kPerToken;
+    const int share_t = threadIdx.x / kPerToken, share_j = threadIdx.x % kPerToken;
+    const bool share_in = share_t < toks && share_j < 32 * NC;
+    [[maybe_unused]] float share[kShare] = {};
+    if constexpr (kLora)
+        if (share_in) lora_share<kPerToken>(lora, t0 + share_t, n0, p.n_out, share_j, share);
 #pragma unroll 1
     for (int st = s_begin; st < s_end; st += D) {
         step(st, 0);
@@ -295,14 +293,14 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
 #pragma unroll
             for (int c = 0; c < NC; ++c)
                 *reinterpret_cast<f32x4*>(&red[(wave * R + t * 16 + m) * S::LD + c * 16 + 4 * q]) = acc[t][c];
-    constexpr bool kLora = std::is_same_v<L, MxLora>;
-    if constexpr (kLora)
-        if (st_tok < toks)
+    if constexpr (kLora) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float both = group_sum<2>(share[i]);
-                if (!(st_j & 1)) red[(kSkinnyWaves * R + st_tok) * S::LD + i * 2 * NC + st_j / 2] = both;
-            }
+        for (int i = 0; i < kShare; ++i) {
+            const float both = group_sum<2>(share[i]);
+            if (share_in && !(share_j & 1))
+                red[(kSkinnyWaves * R + share_t) * S::LD + i * (kPerToken / 2) + share_j / 2] = both;
+        }
+    }
     __syncthreads();
 #pragma unroll 1
     for (int i = threadIdx.x; i < R * 4 * NC; i += kSkinnyThreads) {
