@@ -346,12 +346,27 @@ def mx_proj(x, codes, scales, out, workspace=None, stream=None):
     return out
 
 
-def _on_current_device(*tensors):
-    """The library launches on the current device: operands live there."""
-    dev = _device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{dev}")
+def _current_device():
+    """The device the library launches on; -2, which no tensor is on, without a
+    GPU."""
+    try:
+        return _device()
+    except (RuntimeError, AssertionError, AttributeError):
+        return -2
+
+
+def _fit(dev, t, numel, dtype):
+    """Whether t is a contiguous tensor of this dtype on device `dev` (the
+    current one, where the library launches) with at least numel elements."""
+    return (t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and
+            t.numel() >= numel)
+
+
+def _want(dev, t, name, numel, dtype):
+    """_fit, or the error that says why not; numel 0 accepts anything."""
+    if numel > 0 and not _fit(dev, t, numel, dtype):
+        _need(t, name, numel, dtype)
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
 
 
 def _workspace(ws):
@@ -363,18 +378,18 @@ def _workspace(ws):
     return ws.data_ptr(), ws.nbytes
 
 
-def _lora_args(a, b, scale, token_adapter, n_tok, n_in, n_out):
+def _lora_args(dev, a, b, scale, token_adapter, n_tok, n_in, n_out):
     """Checks the adapters' tensors; their count and rank."""
     if a is None or a.dim() != 3 or a.shape[2] != n_in:
         raise ValueError(f"lora_a: expected [adapters, rank, {n_in}]")
-    n, rank = a.shape[0], a.shape[1]
+    n, rank, _ = a.shape
     if n:
-        _need(a, "lora_a", n * rank * n_in, torch.bfloat16)
         if b is None or b.shape != (n, n_out, rank):
             raise ValueError(f"lora_b: expected [{n}, {n_out}, {rank}]")
-        _need(b, "lora_b", n * n_out * rank, torch.bfloat16)
-        _need(scale, "lora_scale", n, torch.float32)
-        _need(token_adapter, "token_adapter", n_tok, torch.int32)
+        _want(dev, a, "lora_a", n * rank * n_in, torch.bfloat16)
+        _want(dev, b, "lora_b", n * n_out * rank, torch.bfloat16)
+        _want(dev, scale, "lora_scale", n, torch.float32)
+        _want(dev, token_adapter, "token_adapter", n_tok, torch.int32)
     return n, rank
 
 
@@ -397,11 +412,10 @@ def mx_proj_lora(x, codes, scales, lora_a, lora_b, lora_scale, token_adapter, ou
     (n_tok, n_in), n_out = x.shape, out.shape[1]
     ld_x = _rows(x, "x", (n_tok, n_in), torch.bfloat16)
     ld_y = _rows(out, "out", (n_tok, n_out), out.dtype)
-    code = _dtype(out, "out")
-    _need(codes, "codes", n_out * n_in // 2, torch.uint8)
-    _need(scales, "scales", n_out * n_in // GDN_MX_GROUP, torch.uint8)
-    n, rank = _lora_args(lora_a, lora_b, lora_scale, token_adapter, n_tok, n_in, n_out)
-    _on_current_device(out, lora_a, token_adapter)
+    code, dev = _dtype(out, "out"), _current_device()
+    _want(dev, codes, "codes", n_out * n_in // 2, torch.uint8)
+    _want(dev, scales, "scales", n_out * n_in // GDN_MX_GROUP, torch.uint8)
+    n, rank = _lora_args(dev, lora_a, lora_b, lora_scale, token_adapter, n_tok, n_in, n_out)
     ws, ws_bytes = _workspace(workspace)
     _check(lib.gdn_mx_proj_lora(n_tok, n_in, n_out, x.data_ptr(), ld_x, codes.data_ptr(),
                                 scales.data_ptr(), n, rank, _ptr(lora_a), _ptr(lora_b),
@@ -428,7 +442,7 @@ def beam_select(logits, scores, parents, tokens, scores_out, finished=None, fini
     if logits.dim() != 3 or scores_out.dim() != 2:
         raise ValueError("logits: expected [requests, width, vocab], scores_out [requests, n_out]")
     n_req, width, vocab = logits.shape
-    n_out = scores_out.shape[1]
+    n_out, dev = scores_out.shape[1], _current_device()
     code = _dtype(logits, "logits")
     ld = vocab
     if not logits.is_contiguous():
@@ -436,20 +450,21 @@ def beam_select(logits, scores, parents, tokens, scores_out, finished=None, fini
         if (vocab > 1 and logits.stride(2) != 1) or \
                 (n_req > 1 and width > 1 and logits.stride(0) != width * ld):
             raise ValueError("logits: rows are not contiguous and evenly spaced")
-    if not logits.is_cuda:
-        raise ValueError("logits: not a device tensor")
-    for t, name, shape, dt in ((scores, "scores", (n_req, width), torch.float32),
-                               (parents, "parents", (n_req, n_out), torch.int32),
-                               (tokens, "tokens", (n_req, n_out), torch.int32),
-                               (scores_out, "scores_out", (n_req, n_out), torch.float32),
-                               (finished, "finished", (n_req, width), torch.uint8),
-                               (finished_out, "finished_out", (n_req, n_out), torch.uint8)):
-        if t is None and shape and name.startswith("finished"):
-            continue
-        if t is None or t.shape != shape:
-            raise ValueError(f"{name}: expected {shape}")
-        _need(t, name, t.numel(), dt)
-    _on_current_device(logits, scores, parents)
+    if logits.get_device() != dev:
+        _need(logits, "logits", max(1, logits.numel()), logits.dtype)
+        raise ValueError(f"logits: on {logits.device}, but the current device is cuda:{dev}")
+    wide, kept = (n_req, width), (n_req, n_out)
+    for t, name, shape, dt in ((scores, "scores", wide, torch.float32), (parents, "parents", kept, torch.int32),
+                               (tokens, "tokens", kept, torch.int32), (scores_out, "scores_out", kept, torch.float32),
+                               (finished, "finished", wide, torch.uint8),
+                               (finished_out, "finished_out", kept, torch.uint8)):
+        if t is None:
+            if name.startswith("finished"):
+                continue
+            raise ValueError(f"{name}: missing")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+        _want(dev, t, name, shape[0] * shape[1], dt)
     ws, ws_bytes = _workspace(workspace)
     _check(lib.gdn_beam_select(n_req, width, vocab, n_out, code, logits.data_ptr(), ld,
                                scores.data_ptr(), _ptr(finished), eos, parents.data_ptr(),
@@ -541,11 +556,10 @@ class Pool:
         if slots.dim() != 2 or slots.shape != parents.shape or slots.shape != slots_out.shape:
             raise ValueError("slots, parents and slots_out: expected [requests, width]")
         n_req, width = slots.shape
-        n = n_req * width
-        _need(slots, "slots", n, torch.int32)
-        _need(parents, "parents", n, torch.int32)
-        _need(slots_out, "slots_out", n, torch.int32)
-        _on_current_device(slots, parents, slots_out)
+        n, dev = n_req * width, _current_device()
+        _want(dev, slots, "slots", n, torch.int32)
+        _want(dev, parents, "parents", n, torch.int32)
+        _want(dev, slots_out, "slots_out", n, torch.int32)
         _check(lib.gdn_slot_reorder(self._h, n_req, width, slots.data_ptr(), parents.data_ptr(),
                                     slots_out.data_ptr(), _stream(stream)), "gdn_slot_reorder")
         return slots_out
@@ -558,32 +572,34 @@ class Pool:
         share one length, the tokens there is room for; without any, max_tokens
         says it."""
         lib = _lib or load_library()
-        n, room = lens.numel(), max_tokens
+        n, room, dev, i32 = lens.numel(), max_tokens, _current_device(), torch.int32
         for t, name in ((token_seq, "token_seq"), (token_pos, "token_pos"),
                         (token_adapter, "token_adapter")):
             if t is not None:
                 if room is None:
                     room = t.numel()
-                _need(t, name, room, torch.int32)
-                if t.numel() != room:
+                elif t.numel() != room:
                     raise ValueError(f"{name}: {t.numel()} elements, expected {room}")
+                _want(dev, t, name, room, i32)
         if room is None:
             room = 2 ** 31 - 2
         if token_adapter is not None and adapter_ids is None:
             raise ValueError("token_adapter needs adapter_ids")
-        _need(lens, "lens", n, torch.int32)
-        _need(cu_seqlens, "cu_seqlens", n + 1, torch.int32)
-        for t, name in ((last_rows, "last_rows"), (past, "past"), (adapter_ids, "adapter_ids")):
-            if t is not None:
-                _need(t, name, n, torch.int32)
+        _want(dev, lens, "lens", n, i32)
+        _want(dev, cu_seqlens, "cu_seqlens", n + 1, i32)
+        if last_rows is not None:
+            _want(dev, last_rows, "last_rows", n, i32)
+        if past is not None:
+            _want(dev, past, "past", n, i32)
+        if adapter_ids is not None:
+            _want(dev, adapter_ids, "adapter_ids", n, i32)
         n_free = max_ckpt = 0
         if ckpt_every > 0:
-            _need(ckpt_offsets, "ckpt_offsets", n + 1, torch.int32)
+            _want(dev, ckpt_offsets, "ckpt_offsets", n + 1, i32)
             n_free = 0 if free_slots is None else free_slots.numel()
             max_ckpt = 0 if ckpt_slots is None else ckpt_slots.numel()
-            _need(free_slots, "free_slots", n_free, torch.int32)
-            _need(ckpt_slots, "ckpt_slots", max_ckpt, torch.int32)
-        _on_current_device(lens, cu_seqlens, token_seq)
+            _want(dev, free_slots, "free_slots", n_free, i32)
+            _want(dev, ckpt_slots, "ckpt_slots", max_ckpt, i32)
         _check(lib.gdn_batch_maps(self._h, n, _ptr(lens), room, cu_seqlens.data_ptr(), _ptr(last_rows),
                                   _ptr(token_seq), _ptr(past), _ptr(token_pos), _ptr(adapter_ids),
                                   n_adapters, _ptr(token_adapter), ckpt_every, _ptr(free_slots), n_free,
@@ -785,12 +801,12 @@ class Pool:
         """gdn_mx_in_proj_lora: mx_in_proj with a low-rank adapter per token (see
         mx_proj_lora); the gates' logits get theirs before the activation."""
         lib = _lib or load_library()
-        n_tok, hidden = int(x.shape[0]), int(x.shape[1])
+        n_tok, hidden = x.shape
         h_v, kw, vw, io = self.desc.h_v, self._k_width, self._v_width, self.io_torch
-        n_out = self.c_conv + (0 if z is None else vw) + 2 * h_v
-        _need(x, "x", n_tok * hidden, torch.bfloat16)
-        _need(codes, "codes", n_out * hidden // 2, torch.uint8)
-        _need(scales, "scales", n_out * hidden // GDN_MX_GROUP, torch.uint8)
+        n_out, dev = self.c_conv + (0 if z is None else vw) + 2 * h_v, _current_device()
+        _want(dev, x, "x", n_tok * hidden, torch.bfloat16)
+        _want(dev, codes, "codes", n_out * hidden // 2, torch.uint8)
+        _want(dev, scales, "scales", n_out * hidden // GDN_MX_GROUP, torch.uint8)
         if not _hold(n_tok * kw, io, q, k):
             _need(q, "q", n_tok * kw, io)
             _need(k, "k", n_tok * kw, io)
@@ -801,8 +817,7 @@ class Pool:
         if not _hold(n_tok * h_v, torch.float32, a, b):
             _need(a, "a", n_tok * h_v, torch.float32)
             _need(b, "b", n_tok * h_v, torch.float32)
-        n, rank = _lora_args(lora_a, lora_b, lora_scale, token_adapter, n_tok, hidden, n_out)
-        _on_current_device(q, lora_a, token_adapter)
+        n, rank = _lora_args(dev, lora_a, lora_b, lora_scale, token_adapter, n_tok, hidden, n_out)
         ws, ws_bytes = _workspace(workspace)
         _check(lib.gdn_mx_in_proj_lora(self._h, n_tok, hidden, x.data_ptr(), codes.data_ptr(),
                                        scales.data_ptr(), n, rank, _ptr(lora_a), _ptr(lora_b),
