@@ -21,8 +21,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kPer = 8, kStep = kThreads * kPer;  // logits per lane and per step of a workgroup
+constexpr int kPer = 8;                          // logits per lane and step
 constexpr int kHeld = 64 + 64 * kPer;            // keys of a wave that wait, 63 and a step's
 constexpr int kSide = 4;                         // exponentials side by side
 constexpr int kMaxSplits = 64;                   // a lane per stretch when they are put together
@@ -30,6 +29,7 @@ constexpr int kMergeThreads = 512, kMergeWaves = kMergeThreads / 64;
 constexpr float kNone = -__builtin_inff();
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453;
 constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: a sum's low bits are its integer
@@ -214,7 +214,7 @@ struct Stretch {
 };
 
 struct Shape {
-    int rows, width, vocab, n_out, splits, steps;   // steps of 2048 logits to a stretch
+    int rows, width, vocab, n_out, splits, steps, waves;   // steps of 512 logits per wave to a stretch
 };
 
 // Of equal groups of lanes the least of the groups' largest.
@@ -233,11 +233,41 @@ __device__ __forceinline__ float max_number(float a, float b) {
     return r;
 }
 
-// One workgroup per stretch of a row.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void beam_rows_kernel(Shape sh, const T* logits, int64_t ld, const float* scores,
-                                                            const uint8_t* finished, Stretch* stats, uint64_t* keys) {
-    __shared__ u32x2 held[kWaves][kHeld];   // logit and token
+// exp of bf16 values by table: those of magnitudes 2^-13 up to 64, both signs, an
+// entry of 1 for what is smaller (with a correction where it is not 0), and of 0 for
+// what is larger (negative, and far below the row's largest: see where it is used).
+// Looking one up takes about half of computing one.
+struct ExpTable {
+    static constexpr int kFirst = 0x3900, kPast = 0x4280, kSize = kPast - kFirst + 2;   // bits of 2^-13 and 64
+    static constexpr int kBytes = 2 * kSize * 8;
+    static_assert(kBytes < 65536, "byte offsets in 16 bits");
+    static __device__ __forceinline__ void fill(double* t, int thread, int threads) {
+        for (int i = thread; i < 2 * kSize; i += threads) {
+            const int j = i % kSize;
+            const double x = (double)bf16_to_f32((uint16_t)(kFirst - 1 + j));
+            // exp64 takes what is not above 0
+            const double down = exp64(-x);
+            t[i] = j == 0 ? 1.0 : j == kSize - 1 ? 0.0 : i < kSize ? 1.0 / down : down;
+        }
+    }
+    // Byte offsets of two values; the smaller of their places (0: below 2^-13).
+    static __device__ __forceinline__ u16x2 offsets(uint32_t two, u16x2& place) {
+        const u16x2 b = __builtin_bit_cast(u16x2, two), size = {kSize * 8, kSize * 8}, lo = {kFirst - 1, kFirst - 1};
+        const u16x2 m = __builtin_elementwise_max(__builtin_bit_cast(u16x2, two & 0x7fff7fffu), lo) - lo;
+        place = __builtin_elementwise_min(m, u16x2{kSize - 1, kSize - 1});
+        return place * (uint16_t)8 + (b >> (uint16_t)15) * size;
+    }
+};
+
+// One workgroup of W waves per stretch of a row.  TABLE (bf16): exponentials by table
+// where a wave's values allow it.
+template <typename T, int W, bool TABLE>
+__global__ __launch_bounds__(64 * W) void beam_rows_kernel(Shape sh, const T* logits, int64_t ld, const float* scores,
+                                                          const uint8_t* finished, Stretch* stats, uint64_t* keys) {
+    constexpr int kWaves = W, kThreads = 64 * W, kStep = kThreads * kPer;
+    extern __shared__ __align__(16) uint8_t lds[];
+    auto* held = reinterpret_cast<u32x2(*)[kHeld]>(lds);   // [wave]: logit and token
+    [[maybe_unused]] auto* table = reinterpret_cast<double*>(lds + sizeof(u32x2) * kHeld * kWaves);
     __shared__ uint64_t list[64];
     __shared__ int kept[2][kWaves];   // of even and odd steps: the last step's may still be read
     __shared__ double sums[kWaves], tops[kWaves];
@@ -251,6 +281,7 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(Shape sh, const T* 
     next.load(x_row, begin + (int)threadIdx.x * kPer, sh.vocab);
     // a beam without continuations, or with one that needs no logits
     if (!(fabsf(scores[row]) <= FLT_MAX) || (finished && finished[row])) return;
+    if constexpr (TABLE) ExpTable::fill(table, threadIdx.x, kThreads);   // a barrier follows in the first step
     // lanes to a part, for the first bound: parts of one wave, of all waves
     const int alone = 64 >> (sh.n_out > 1 ? 32 - __builtin_clz(sh.n_out - 1) : 0);
     const int group = min(64, alone * kWaves);
@@ -258,22 +289,25 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(Shape sh, const T* 
     // where |c| is large, x is first made x - base in fp32, exact where it counts.
     float c = -FLT_MAX, base = c, least = kNone;   // least: the list's last key that counts
     double shift = kMagic, sum = 0.0;
+    [[maybe_unused]] bool by_table = false;   // the wave's largest is -20 to 64 so far, and c is 0
     int n = 0, joins = 0, odd = 0;
     for (int i = begin; i < end; i += kStep) {
         float x[kPer];
         const int at = i + (int)threadIdx.x * kPer;
+        const Eight<T> now = next;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) x[k] = Io<T>::load(next.v, k);
+        for (int k = 0; k < kPer; ++k) x[k] = Io<T>::load(now.v, k);
         if (i + kStep < end) next.load(x_row, at + kStep, sh.vocab);
         // infinities and NaN are always above and always far
-        const float reach = c + 600.0f, bar = fminf(least, reach);
-        uint64_t above = 0;
+        const float reach = TABLE && by_table ? 63.75f : c + 600.0f, bar = fminf(least, reach);
+        uint64_t above[kPer], some = 0;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) above |= __ballot(!(x[k] <= bar));
-        if (above || i == begin) {
+        for (int k = 0; k < kPer; ++k) some |= above[k] = __ballot(!(x[k] <= bar));
+        if (some || i == begin) {
             uint64_t far = 0;
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) far |= __ballot(!(x[k] <= reach));
+            for (int k = 0; k < kPer; ++k)
+                if (above[k]) far |= __ballot(!(x[k] <= reach));
             if (far || i == begin) {
 #pragma unroll
                 for (int k = 0; k < kPer; ++k) x[k] = x[k] != x[k] ? kNone : fminf(x[k], FLT_MAX);
@@ -283,6 +317,8 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(Shape sh, const T* 
                 if (__any(top > reach)) {   // also the first time, unless nothing is above the lowest value
                     const double old = (double)base + (kMagic - shift) * kLn2;
                     c = all_max(top);
+                    by_table = TABLE && c >= -20.0f && c < 64.0f;
+                    if (by_table) c = 0.0f;
                     const double ints = rint((double)c * kLog2e);
                     base = fabsf(c) > 1e5f ? c : 0.0f;
                     shift = fabsf(c) > 1e5f ? kMagic : kMagic - ints;
@@ -307,34 +343,59 @@ __global__ __launch_bounds__(kThreads) void beam_rows_kernel(Shape sh, const T* 
             // Equal to the list's last is not enough: tokens are higher here.
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
+                if (!above[k] && i != begin) continue;
                 const uint64_t mask = __ballot(x[k] > least);
-                if (mask) {
-                    const uint32_t to = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
-                                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
-                    if (x[k] > least) held[wave][to] = u32x2{__float_as_uint(x[k]), (uint32_t)(at + k)};
-                    n += __popcll(mask);
-                }
+                const uint32_t to = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                              __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
+                if (x[k] > least) held[wave][to] = u32x2{__float_as_uint(x[k]), (uint32_t)(at + k)};
+                n += __popcll(mask);
             }
         }
         odd ^= 1;
         if (lane == 0) kept[odd][wave] = n;
-        if (base != 0.0f) {
+        if (TABLE && by_table) {
+            if constexpr (TABLE) {
+                uint32_t two[kPer / 2];
+                __builtin_memcpy(two, now.v, sizeof two);
+                u16x2 least_place = {0xffff, 0xffff};
+                double e[kPer];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) x[k] = x[k] - base;
-        }
-        const float low = c - base - 700.0f;
+                for (int k = 0; k < kPer; k += 2) {
+                    u16x2 place;
+                    const u16x2 at2 = ExpTable::offsets(two[k / 2], place);
+                    least_place = __builtin_elementwise_min(least_place, place);
+                    e[k] = *reinterpret_cast<const double*>(reinterpret_cast<const char*>(table) + at2[0]);
+                    e[k + 1] = *reinterpret_cast<const double*>(reinterpret_cast<const char*>(table) + at2[1]);
+                }
 #pragma unroll
-        for (int k0 = 0; k0 < kPer; k0 += kSide) {
-            double m[kSide], r[kSide], e[kSide];
+                for (int k = 0; k < kPer; ++k) sum += e[k];
+                if (__any(least_place[0] == 0 || least_place[1] == 0)) {
 #pragma unroll
-            for (int k = 0; k < kSide; ++k) {
-                const double d = (double)max_number(x[k0 + k], low);
-                m[k] = fma(d, kLog2e, shift);
-                r[k] = fma(m[k] - shift, -kLn2, d);
+                    for (int k = 0; k < kPer; ++k) {   // exp(x) - 1 of magnitudes below 2^-13
+                        const double d = fabsf(x[k]) < 0x1p-13f ? (double)x[k] : 0.0;
+                        sum += fma(d * d, fma(d, 1.0 / 6.0, 0.5), d);
+                    }
+                }
             }
-            exp_scaled(r, m, e);
+        } else {
+            if (base != 0.0f) {
 #pragma unroll
-            for (int k = 0; k < kSide; ++k) sum += e[k];
+                for (int k = 0; k < kPer; ++k) x[k] = x[k] - base;
+            }
+            const float low = c - base - 700.0f;
+#pragma unroll
+            for (int k0 = 0; k0 < kPer; k0 += kSide) {
+                double m[kSide], r[kSide], e[kSide];
+#pragma unroll
+                for (int k = 0; k < kSide; ++k) {
+                    const double d = (double)max_number(x[k0 + k], low);
+                    m[k] = fma(d, kLog2e, shift);
+                    r[k] = fma(m[k] - shift, -kLn2, d);
+                }
+                exp_scaled(r, m, e);
+#pragma unroll
+                for (int k = 0; k < kSide; ++k) sum += e[k];
+            }
         }
         __syncthreads();
         int total = 0;
@@ -443,40 +504,62 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
         finished_out[at] = some && ((finished && finished[req * sh.width + parent]) || tok == eos);
 }
 
-// Stretches: enough waves for the card, at most a lane's worth, none empty.
-Shape beam_shape(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out) {
-    const int rows = n_req * width, steps = (vocab + kStep - 1) / kStep;
-    const int want = std::max(1, std::min({kMaxSplits, steps, 2048 / std::max(1, rows)}));
+// Stretches: enough workgroups for the card, at most a lane's worth, none empty.
+Shape beam_shape(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, int waves, int wanted) {
+    const int rows = n_req * width, step = waves * 64 * kPer, steps = (vocab + step - 1) / step;
+    const int want = std::max(1, std::min({kMaxSplits, steps, wanted / std::max(1, rows)}));
     const int per = (steps + want - 1) / want;
-    return {rows, width, vocab, n_out, (steps + per - 1) / per, per};
+    return {rows, width, vocab, n_out, (steps + per - 1) / per, per, waves};
+}
+
+// Workgroups of eight waves with the table, two to a CU, where each has eight steps or
+// more to fill it for; of four waves otherwise.
+Shape beam_plan(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype) {
+    const Shape s = beam_shape(n_req, width, vocab, n_out, 8, 512);
+    return dtype == GDN_BF16 && s.steps >= 8 ? s : beam_shape(n_req, width, vocab, n_out, 4, 2048);
 }
 
 size_t stats_bytes(const Shape& s) {
     return ((size_t)s.rows * s.splits * sizeof(Stretch) + 255) / 256 * 256;
 }
 
+template <typename T, int W, bool TABLE>
+hipError_t launch_rows(const Shape& s, const void* logits, int64_t ld, const float* scores, const uint8_t* finished,
+                       Stretch* stats, uint64_t* keys, hipStream_t stream) {
+    constexpr int lds = sizeof(u32x2) * kHeld * W + (TABLE ? ExpTable::kBytes : 0);
+    if (lds > 60000) {
+        static std::atomic<uint64_t> done{0};
+        const hipError_t e = allow_dynamic_lds(&beam_rows_kernel<T, W, TABLE>, lds, &done);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((beam_rows_kernel<T, W, TABLE>), dim3((unsigned)(s.rows * s.splits)), dim3(64 * W), lds, stream, s,
+                       static_cast<const T*>(logits), ld, scores, finished, stats, keys);
+    return hipGetLastError();
+}
+
 }  // namespace
 
+// Enough for either type.
 size_t beam_select_workspace_bytes(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out) {
-    const Shape s = beam_shape(n_req, width, vocab, n_out);
-    return stats_bytes(s) + (size_t)s.rows * s.splits * n_out * sizeof(uint64_t);
+    size_t most = 0;
+    for (const gdn_dtype t : {GDN_F32, GDN_BF16}) {
+        const Shape s = beam_plan(n_req, width, vocab, n_out, t);
+        most = std::max(most, stats_bytes(s) + (size_t)s.rows * s.splits * n_out * sizeof(uint64_t));
+    }
+    return most;
 }
 
 hipError_t launch_beam_select(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype,
                               const void* logits, int64_t ld, const float* scores, const uint8_t* finished,
                               int32_t eos, int32_t* parents, int32_t* tokens, float* scores_out,
                               uint8_t* finished_out, void* workspace, hipStream_t stream) {
-    const Shape s = beam_shape(n_req, width, vocab, n_out);
+    const Shape s = beam_plan(n_req, width, vocab, n_out, dtype);
     Stretch* stats = static_cast<Stretch*>(workspace);
     uint64_t* keys = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + stats_bytes(s));
-    const dim3 grid((unsigned)(s.rows * s.splits));
-    if (dtype == GDN_BF16)
-        hipLaunchKernelGGL(beam_rows_kernel<uint16_t>, grid, dim3(kThreads), 0, stream, s,
-                           static_cast<const uint16_t*>(logits), ld, scores, finished, stats, keys);
-    else
-        hipLaunchKernelGGL(beam_rows_kernel<float>, grid, dim3(kThreads), 0, stream, s,
-                           static_cast<const float*>(logits), ld, scores, finished, stats, keys);
-    hipError_t e = hipGetLastError();
+    const hipError_t e =
+        dtype == GDN_F32 ? launch_rows<float, 4, false>(s, logits, ld, scores, finished, stats, keys, stream)
+        : s.waves == 4   ? launch_rows<uint16_t, 4, false>(s, logits, ld, scores, finished, stats, keys, stream)
+                         : launch_rows<uint16_t, 8, true>(s, logits, ld, scores, finished, stats, keys, stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(beam_merge_kernel, dim3(n_req), dim3(kMergeThreads), 0, stream, s, stats, keys, scores,
                        finished, eos, parents, tokens, scores_out, finished_out);

@@ -118,6 +118,42 @@ def test_equal_logits_far_apart_in_a_long_row(G, seed):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("v", [33001, 70000])
+def test_many_long_rows_of_every_kind(G, v, dtype):
+    """Enough rows that a workgroup takes a long stretch: logits of many sizes,
+    zeros, tiny ones, far ones early and late in a row, masks, infinities and NaN."""
+    gen = _gen(v)
+    x = _logits(gen, 66, 8, v, F32)
+    x[0] *= 1.0e-6
+    x[1] *= 2.0e-4
+    x[2] *= 20.0
+    x[3] *= 300.0
+    x[4] -= 30.0
+    x[5] -= 90.0
+    x[6] += 70.0
+    x[7, :, ::2] = 0.0
+    x[8, :, 100:] = -0.0
+    x[9, :, v - 3] = 64.0
+    x[10, :, v - 3] = 700.0
+    x[11, :, v // 2] = -700.0
+    x[12, :, 5000:] = -math.inf
+    x[13, :, :5000] = -math.inf
+    x[14, :, 7::5] = math.nan
+    x[15, :, v - 9] = math.inf
+    x[16] = -math.inf
+    x[17, :, ::3] = torch.finfo(dtype).min
+    x[18] = -19.0 - x[18].abs()
+    x[19] = -20.5 - x[19].abs()
+    x[20, :, :20000] -= 1000.0
+    x[21, :, 20000:] += 1000.0
+    x[22] *= 1.0e30
+    x[23] = 2.0 ** -13
+    x[24] = -63.9
+    x[25, :, 1:] = -64.0
+    _check(G, x.to(dtype), -torch.rand(66, 8, generator=torch.Generator().manual_seed(v)) * 8, 8)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("k", [1, 5, 64])
 def test_rising_and_falling_rows(G, dtype, k):
     """Every element of a rising row beats those before it."""
