@@ -25,7 +25,8 @@ constexpr int kPer = 8;                          // logits per lane and step
 constexpr int kHeld = 64 + 64 * kPer;            // keys of a wave that wait, 63 and a step's
 constexpr int kSide = 4;                         // exponentials side by side
 constexpr int kMaxSplits = 64;                   // a lane per stretch when they are put together
-constexpr int kMergeThreads = 512, kMergeWaves = kMergeThreads / 64;
+constexpr int kMergeThreads = 1024, kMergeWaves = kMergeThreads / 64;
+constexpr int kBatch = 4;                        // loads of 64 keys at a time
 constexpr float kNone = -__builtin_inff();
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -207,6 +208,12 @@ struct Eight {
         }
     }
 };
+
+// A wave's own places of LDS: what its lanes wrote is there for all of them.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
 // What a stretch of a row leaves: the sum of exp(x - c), beside its best keys.
 struct Stretch {
@@ -438,16 +445,16 @@ __global__ __launch_bounds__(64 * W) void beam_rows_kernel(Shape sh, const T* lo
     if (wave == 0 && lane < sh.n_out) keys[(int64_t)blockIdx.x * sh.n_out + lane] = list[lane];
 }
 
-// One workgroup per request: each wave puts the stretches of its beams together,
-// then one the waves' lists.
+// One workgroup per request: each wave puts the stretches of its beams together, then
+// half of the waves' lists go into the other half's at a time.
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, const Stretch* stats, const uint64_t* keys,
                                                                   const float* scores, const uint8_t* finished, int eos,
                                                                   int32_t* parents, int32_t* tokens, float* scores_out,
                                                                   uint8_t* finished_out) {
-    __shared__ uint64_t l_score[kMergeWaves][64];
-    __shared__ uint32_t l_tag[kMergeWaves][64];
+    __shared__ uint64_t held[kMergeWaves][128], l_score[kMergeWaves / 2][64];
+    __shared__ uint32_t l_tag[kMergeWaves / 2][64];
     __shared__ int32_t token[GDN_BEAM_MAX * GDN_BEAM_MAX];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t req = blockIdx.x;
     Entry mine{0, ~0u};
     for (int b = wave; b < sh.width; b += kMergeWaves) {
@@ -455,8 +462,11 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
         // all loads at once; what a beam without logits has there is not looked at
         const int count = sh.splits * sh.n_out;
         const uint64_t* from = keys + row * count;
+        // the lists' first keys come first
         const auto key_at = [&](int i) { return i < count ? from[i % sh.splits * sh.n_out + i / sh.splits] : 0; };
-        uint64_t key = key_at(lane);
+        uint64_t key[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) key[j] = key_at(j * 64 + lane);
         const Stretch st = lane < sh.splits ? stats[row * sh.splits + lane] : Stretch{-HUGE_VAL, 0.0};
         const float base = scores[row];
         const bool done = finished && finished[row];
@@ -473,13 +483,37 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
             // One lane's sum for all: equal logits need equal scores.  Apart from c, beside
             // which the logarithm would be lost where logits reach 1e38.
             const double norm = log(__builtin_bit_cast(double, read_lane(__builtin_bit_cast(uint64_t, sum), 0)));
-            // The lists are sorted: their first keys come first, and few others pass.
-            uint64_t best = sort64(key);
-            for (int i = 64; i < count; i += 64) {
-                key = key_at(i + lane);
-                if (!__any(key > read_lane(best, sh.n_out - 1))) break;   // every list has a key here: none further down is larger
-                best = merge64(best, sort64(key));
+            // The lists are sorted, so few keys but the first pass; they wait in LDS for
+            // a sort of 64.  Where none of 64 passes, every list has one, and none further
+            // down is larger.
+            uint64_t best = sort64(key[0]), bar = read_lane(best, sh.n_out - 1);
+            int n = 0;
+            const auto join = [&]() {
+                wave_sync();
+                best = merge64(best, sort64(lane < n ? held[wave][lane] : 0));
+                bar = read_lane(best, sh.n_out - 1);
+                const uint64_t rest = 64 + lane < n ? held[wave][64 + lane] : 0;
+                wave_sync();
+                held[wave][lane] = rest;
+                n = max(n - 64, 0);
+            };
+            bool more = true;
+            for (int i = 64; i < count && more; i += 64 * kBatch) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) key[j] = j + 1 < kBatch && i == 64 ? key[j + 1] : key_at(i + j * 64 + lane);
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const uint64_t mask = __ballot(key[j] > bar);
+                    more = more && mask;
+                    if (!more) continue;
+                    const uint32_t to = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)mask, n));
+                    if (key[j] > bar) held[wave][to] = key[j];
+                    n += __popcll(mask);
+                    if (n >= 64) join();
+                }
             }
+            if (n > 0) join();
             if (best && lane < sh.n_out) {
                 e.score = image((double)base +
                                 (((double)image_value((uint32_t)(best >> 32)) - c) - norm));
@@ -488,12 +522,18 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
         }
         mine = merge64(mine, e);
     }
-    l_score[wave][lane] = mine.score;
-    l_tag[wave][lane] = mine.tag;
-    __syncthreads();
-    if (wave != 0) return;
-    for (int w = 1; w < min(kMergeWaves, sh.width); ++w) mine = merge64(mine, Entry{l_score[w][lane], l_tag[w][lane]});
-    if (lane >= sh.n_out) return;
+#pragma unroll
+    for (int w = kMergeWaves / 2; w > 0; w /= 2) {
+        if (w >= sh.width) continue;   // waves without a beam
+        if (wave >= w && wave < 2 * w) {
+            l_score[wave - w][lane] = mine.score;
+            l_tag[wave - w][lane] = mine.tag;
+        }
+        __syncthreads();
+        if (wave < w) mine = merge64(mine, Entry{l_score[wave][lane], l_tag[wave][lane]});
+        __syncthreads();
+    }
+    if (wave != 0 || lane >= sh.n_out) return;
     const int64_t at = req * sh.n_out + lane;
     const bool some = mine.score != 0;
     const int parent = some ? (int)(mine.tag / 64) : -1, tok = some ? token[mine.tag] : -1;
@@ -516,7 +556,7 @@ Shape beam_shape(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, int
 // more to fill it for; of four waves otherwise.
 Shape beam_plan(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype) {
     const Shape s = beam_shape(n_req, width, vocab, n_out, 8, 512);
-    return dtype == GDN_BF16 && s.steps >= 8 ? s : beam_shape(n_req, width, vocab, n_out, 4, 2048);
+    return dtype == GDN_BF16 && s.steps >= 8 ? s : beam_shape(n_req, width, vocab, n_out, 4, 1024);
 }
 
 size_t stats_bytes(const Shape& s) {
