@@ -80,9 +80,6 @@ __device__ __forceinline__ uint64_t image(double x) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
     return u ^ ((uint64_t)((int64_t)u >> 63) | (uint64_t)1 << 63);
 }
-__device__ __forceinline__ double image_value(uint64_t k) {
-    return __builtin_bit_cast(double, k ^ (k >> 63 ? (uint64_t)1 << 63 : ~(uint64_t)0));
-}
 
 // A logit and its token: larger logits first, of equal ones the lower token.  0: none
 // (-infinity and NaN); +infinity counts as the largest finite value.
@@ -90,11 +87,12 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t token) {
     return x > kNone ? (uint64_t)image(fminf(x, FLT_MAX)) << 32 | (uint32_t)~token : 0;
 }
 
-// A continuation: its score's image (0: none), beam * 64 + place in the beam's list.
-struct Entry {
-    uint64_t score;
-    uint32_t tag;
-};
+// A continuation: its score's image to 52 bits, then beam * 64 + place in the beam's
+// list, the lower the better: scores within 2^-40 of their size count as equal.
+// 0: none.
+__device__ __forceinline__ uint64_t entry_of(double score, uint32_t tag) {
+    return (image(score) & ~(uint64_t)0xfff) | (0xfff - tag);
+}
 
 // The value of lane (this ^ MASK).  Inside rows of 16 lanes by DPP, across them by the
 // row and half swaps: a sort of 64 keys makes no trip through LDS.
@@ -125,43 +123,49 @@ template <int MASK>
 __device__ __forceinline__ uint64_t across(uint64_t v) {
     return (uint64_t)across<MASK>((uint32_t)(v >> 32)) << 32 | across<MASK>((uint32_t)v);
 }
-template <int MASK>
-__device__ __forceinline__ Entry across(Entry v) {
-    return {across<MASK>(v.score), across<MASK>(v.tag)};
-}
-__device__ __forceinline__ bool better(uint64_t a, uint64_t b) { return a > b; }
-__device__ __forceinline__ bool better(Entry a, Entry b) {
-    return a.score > b.score || (a.score == b.score && a.tag < b.tag);
-}
-
 // One step of a sorting network: of lanes MASK apart, the one whose bit BIT is clear
 // keeps the better value.
-template <int MASK, int BIT, typename V>
-__device__ __forceinline__ V exchange(V v) {
-    const V o = across<MASK>(v);
-    return better(o, v) == !(threadIdx.x & BIT) ? o : v;
+template <int MASK, int BIT>
+__device__ __forceinline__ uint64_t exchange(uint64_t v) {
+    const uint64_t o = across<MASK>(v);
+    return (o > v) == !(threadIdx.x & BIT) ? o : v;
 }
 
 // Sorts groups of 2 W lanes whose values rise and then fall, or the like.
-template <int W, typename V>
-__device__ __forceinline__ V settle(V v) {
+template <int W>
+__device__ __forceinline__ uint64_t settle(uint64_t v) {
     if constexpr (W > 0) return settle<W / 2>(exchange<W, W>(v));
     else return v;
 }
 
 // The wave's 64 values, best in lane 0.
-template <int W = 2, typename V>
-__device__ __forceinline__ V sort64(V v) {
+template <int W = 2>
+__device__ __forceinline__ uint64_t sort64(uint64_t v) {
     v = settle<W / 4>(exchange<W - 1, W / 2>(v));
     if constexpr (W < 64) return sort64<2 * W>(v);
     else return v;
 }
 
 // The best 64 of two sorted lists, sorted.
-template <typename V>
-__device__ __forceinline__ V merge64(V a, V b) {
-    const V o = across<63>(b);
-    return settle<32>(better(o, a) ? o : a);
+__device__ __forceinline__ uint64_t merge64(uint64_t a, uint64_t b) {
+    const uint64_t o = across<63>(b);
+    return settle<32>(o > a ? o : a);
+}
+
+// The best 64 of the lists of waves 0 to `waves` - 1 (sorted), in wave 0: half of them
+// go into the other half at a time.  By all waves of the workgroup.
+template <int W>
+__device__ __forceinline__ uint64_t merge_waves(uint64_t v, uint64_t (*lists)[64], int waves) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int w = W / 2; w > 0; w /= 2) {
+        if (w >= waves) continue;
+        if (wave >= w && wave < 2 * w) lists[wave - w][lane] = v;
+        __syncthreads();
+        if (wave < w) v = merge64(v, lists[wave][lane]);
+        __syncthreads();
+    }
+    return v;
 }
 
 // Sum and maximum over the wave, in every lane (the lanes' sums a rounding apart
@@ -275,7 +279,7 @@ __global__ __launch_bounds__(64 * W) void beam_rows_kernel(Shape sh, const T* lo
     extern __shared__ __align__(16) uint8_t lds[];
     auto* held = reinterpret_cast<u32x2(*)[kHeld]>(lds);   // [wave]: logit and token
     [[maybe_unused]] auto* table = reinterpret_cast<double*>(lds + sizeof(u32x2) * kHeld * kWaves);
-    __shared__ uint64_t list[64];
+    __shared__ uint64_t list[64], lists[kWaves / 2][64];
     __shared__ int kept[2][kWaves];   // of even and odd steps: the last step's may still be read
     __shared__ double sums[kWaves], tops[kWaves];
     __shared__ float2 bounds[kWaves];
@@ -409,16 +413,26 @@ __global__ __launch_bounds__(64 * W) void beam_rows_kernel(Shape sh, const T* lo
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) total += kept[odd][w];
         if (total < 64 && i != begin && i + kStep < end) continue;
-        // the waves take turns at the list
-        if (wave == joins % kWaves) {
-            uint64_t best = joins ? list[lane] : 0;
-            // place lane + 64 j of the waves' keys, one behind the other
-            for (int from = 0; from < total; from += 64) {
-                int w = 0, to = from + lane;
+        // A few keys one wave sorts, the waves in turn; more every wave its own.
+        const bool many = total > 64;
+        uint64_t best = 0;
+        if (many) {
+            for (int from = 0; from < n; from += 64) {
+                const u32x2 e = from + lane < n ? held[wave][from + lane] : u32x2{__float_as_uint(kNone), 0};
+                const uint64_t v = sort64(key_of(__uint_as_float(e[0]), e[1]));
+                best = from ? merge64(best, v) : v;
+            }
+            best = merge_waves<kWaves>(best, lists, kWaves);
+        }
+        if (wave == (many ? 0 : joins % kWaves)) {
+            if (!many) {
+                // place lane of the waves' keys, one behind the other
+                int w = 0, to = lane;
                 while (w < kWaves && to >= kept[odd][w]) to -= kept[odd][w++];
                 const u32x2 e = w < kWaves ? held[w][to] : u32x2{__float_as_uint(kNone), 0};
-                best = merge64(best, sort64(key_of(__uint_as_float(e[0]), e[1])));
+                best = sort64(key_of(__uint_as_float(e[0]), e[1]));
             }
+            if (joins) best = merge64(best, list[lane]);
             list[lane] = best;
             const uint32_t high = (uint32_t)(read_lane(best, sh.n_out - 1) >> 32);
             if (lane == 0) last = high ? image_value(high) : kNone;
@@ -451,12 +465,14 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
                                                                   const float* scores, const uint8_t* finished, int eos,
                                                                   int32_t* parents, int32_t* tokens, float* scores_out,
                                                                   uint8_t* finished_out) {
-    __shared__ uint64_t held[kMergeWaves][128], l_score[kMergeWaves / 2][64];
-    __shared__ uint32_t l_tag[kMergeWaves / 2][64];
+    __shared__ uint64_t held[kMergeWaves][128];
     __shared__ int32_t token[GDN_BEAM_MAX * GDN_BEAM_MAX];
+    __shared__ float logit[GDN_BEAM_MAX * GDN_BEAM_MAX];
+    __shared__ double norms[GDN_BEAM_MAX][2];
+    auto* lists = reinterpret_cast<uint64_t(*)[64]>(held);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t req = blockIdx.x;
-    Entry mine{0, ~0u};
+    uint64_t mine = 0;
     for (int b = wave; b < sh.width; b += kMergeWaves) {
         const int64_t row = req * sh.width + b;
         // all loads at once; what a beam without logits has there is not looked at
@@ -471,11 +487,14 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
         const float base = scores[row];
         const bool done = finished && finished[row];
         if (!(fabsf(base) <= FLT_MAX)) continue;
-        Entry e{0, (uint32_t)(b * 64 + lane)};
-        if (done) {
+        const uint32_t tag = b * 64 + lane;
+        uint64_t e = 0;
+        if (done) {   // as a logit of 0 with nothing to subtract
             if (lane == 0) {
-                e.score = image((double)base);
-                token[b * 64] = eos;
+                e = entry_of((double)base, tag);
+                token[tag] = eos;
+                logit[tag] = 0.0f;
+                norms[b][0] = norms[b][1] = 0.0;
             }
         } else {
             const double c = all_max(st.c);
@@ -486,7 +505,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
             // The lists are sorted, so few keys but the first pass; they wait in LDS for
             // a sort of 64.  Where none of 64 passes, every list has one, and none further
             // down is larger.
-            uint64_t best = sort64(key[0]), bar = read_lane(best, sh.n_out - 1);
+            uint64_t best = sh.splits > 1 ? sort64(key[0]) : key[0], bar = read_lane(best, sh.n_out - 1);
             int n = 0;
             const auto join = [&]() {
                 wave_sync();
@@ -515,31 +534,29 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
             }
             if (n > 0) join();
             if (best && lane < sh.n_out) {
-                e.score = image((double)base +
-                                (((double)image_value((uint32_t)(best >> 32)) - c) - norm));
-                token[b * 64 + lane] = (int32_t)~(uint32_t)best;
+                logit[tag] = image_value((uint32_t)(best >> 32));
+                token[tag] = (int32_t)~(uint32_t)best;
+                e = entry_of((double)base + (((double)logit[tag] - c) - norm), tag);
+            }
+            if (lane == 0) {
+                norms[b][0] = c;
+                norms[b][1] = norm;
             }
         }
-        mine = merge64(mine, e);
+        mine = b < kMergeWaves ? e : merge64(mine, e);
     }
-#pragma unroll
-    for (int w = kMergeWaves / 2; w > 0; w /= 2) {
-        if (w >= sh.width) continue;   // waves without a beam
-        if (wave >= w && wave < 2 * w) {
-            l_score[wave - w][lane] = mine.score;
-            l_tag[wave - w][lane] = mine.tag;
-        }
-        __syncthreads();
-        if (wave < w) mine = merge64(mine, Entry{l_score[wave][lane], l_tag[wave][lane]});
-        __syncthreads();
-    }
+    __syncthreads();   // held is free
+    mine = merge_waves<kMergeWaves>(mine, lists, sh.width);
     if (wave != 0 || lane >= sh.n_out) return;
     const int64_t at = req * sh.n_out + lane;
-    const bool some = mine.score != 0;
-    const int parent = some ? (int)(mine.tag / 64) : -1, tok = some ? token[mine.tag] : -1;
+    const bool some = mine != 0;
+    const int tag = some ? 0xfff - (int)(mine & 0xfff) : 0;
+    const int parent = some ? tag / 64 : -1, tok = some ? token[tag] : -1;
     parents[at] = parent;
     tokens[at] = tok;
-    scores_out[at] = some ? (float)image_value(mine.score) : kNone;
+    scores_out[at] = some ? (float)((double)scores[req * sh.width + parent] +
+                                    (((double)logit[tag] - norms[parent][0]) - norms[parent][1]))
+                          : kNone;
     if (finished_out)
         finished_out[at] = some && ((finished && finished[req * sh.width + parent]) || tok == eos);
 }
