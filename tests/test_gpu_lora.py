@@ -226,7 +226,7 @@ def test_without_adapters_and_without_tokens(G):
     G.mx_proj_lora(x[:0], codes, scales, t(1, 16, 64), t(1, 50, 16), t(1, dt=F32), t(0, dt=torch.int32), y2[:0])
 
 
-@pytest.mark.parametrize("n_tok", [1, 40, 300])
+@pytest.mark.parametrize("n_tok", [1, 40, 300, 1000])
 def test_repeats_on_another_stream_and_in_a_graph(G, n_tok):
     n_in, n_out, rank = 512, 700, 16
     x, codes, scales, a, b, s, ids, _ = _case(G, n_tok, n_in, n_out, rank, 4, "mixed", BF)
