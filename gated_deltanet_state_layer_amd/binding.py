@@ -366,15 +366,22 @@ def _want(dev, t, name, numel, dtype):
     """_fit, or the error that says why not; numel 0 accepts anything."""
     if numel > 0 and not _fit(dev, t, numel, dtype):
         _need(t, name, numel, dtype)
+        _here(dev, t, name)
+
+
+def _here(dev, t, name):
+    """A tensor that is not on device `dev` is an error."""
+    if t.get_device() != dev and t.numel() > 0:
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
 
 
-def _workspace(ws):
+def _workspace(dev, ws):
     """A workspace's pointer and bytes."""
     if ws is None:
         return None, 0
     if not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("workspace: not a contiguous device tensor")
+    _here(dev, ws, "workspace")
     return ws.data_ptr(), ws.nbytes
 
 
@@ -413,10 +420,12 @@ def mx_proj_lora(x, codes, scales, lora_a, lora_b, lora_scale, token_adapter, ou
     ld_x = _rows(x, "x", (n_tok, n_in), torch.bfloat16)
     ld_y = _rows(out, "out", (n_tok, n_out), out.dtype)
     code, dev = _dtype(out, "out"), _current_device()
+    _here(dev, x, "x")
+    _here(dev, out, "out")
     _want(dev, codes, "codes", n_out * n_in // 2, torch.uint8)
     _want(dev, scales, "scales", n_out * n_in // GDN_MX_GROUP, torch.uint8)
     n, rank = _lora_args(dev, lora_a, lora_b, lora_scale, token_adapter, n_tok, n_in, n_out)
-    ws, ws_bytes = _workspace(workspace)
+    ws, ws_bytes = _workspace(dev, workspace)
     _check(lib.gdn_mx_proj_lora(n_tok, n_in, n_out, x.data_ptr(), ld_x, codes.data_ptr(),
                                 scales.data_ptr(), n, rank, _ptr(lora_a), _ptr(lora_b),
                                 _ptr(lora_scale), _ptr(token_adapter), code, out.data_ptr(), ld_y, ws,
@@ -452,7 +461,7 @@ def beam_select(logits, scores, parents, tokens, scores_out, finished=None, fini
             raise ValueError("logits: rows are not contiguous and evenly spaced")
     if logits.get_device() != dev:
         _need(logits, "logits", max(1, logits.numel()), logits.dtype)
-        raise ValueError(f"logits: on {logits.device}, but the current device is cuda:{dev}")
+        _here(dev, logits, "logits")
     wide, kept = (n_req, width), (n_req, n_out)
     for t, name, shape, dt in ((scores, "scores", wide, torch.float32), (parents, "parents", kept, torch.int32),
                                (tokens, "tokens", kept, torch.int32), (scores_out, "scores_out", kept, torch.float32),
@@ -465,7 +474,7 @@ def beam_select(logits, scores, parents, tokens, scores_out, finished=None, fini
         if t.shape != shape:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
         _want(dev, t, name, shape[0] * shape[1], dt)
-    ws, ws_bytes = _workspace(workspace)
+    ws, ws_bytes = _workspace(dev, workspace)
     _check(lib.gdn_beam_select(n_req, width, vocab, n_out, code, logits.data_ptr(), ld,
                                scores.data_ptr(), _ptr(finished), eos, parents.data_ptr(),
                                tokens.data_ptr(), scores_out.data_ptr(), _ptr(finished_out), ws,
@@ -817,8 +826,11 @@ class Pool:
         if not _hold(n_tok * h_v, torch.float32, a, b):
             _need(a, "a", n_tok * h_v, torch.float32)
             _need(b, "b", n_tok * h_v, torch.float32)
+        for t, name in ((q, "q"), (k, "k"), (v, "v"), (a, "a"), (b, "b"), (z, "z")):
+            if t is not None:
+                _here(dev, t, name)
         n, rank = _lora_args(dev, lora_a, lora_b, lora_scale, token_adapter, n_tok, hidden, n_out)
-        ws, ws_bytes = _workspace(workspace)
+        ws, ws_bytes = _workspace(dev, workspace)
         _check(lib.gdn_mx_in_proj_lora(self._h, n_tok, hidden, x.data_ptr(), codes.data_ptr(),
                                        scales.data_ptr(), n, rank, _ptr(lora_a), _ptr(lora_b),
                                        _ptr(lora_scale), _ptr(token_adapter), _ptr(q), _ptr(k), _ptr(v),

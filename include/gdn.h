@@ -194,9 +194,9 @@ gdn_status gdn_slot_reorder(gdn_pool* pool, int32_t n_req, int32_t width, const 
  * Sorted by falling score; of equal scores the lower beam comes first, then the
  * larger logit, then the lower token.  Sums and scores are held in 64 bits; of
  * different beams, scores closer than 2^-40 of their size count as equal.  With
- * fewer continuations
- * than n_out the rest gets parent and token -1, score -infinity, finished 0.  No two
- * of the outputs may overlap, nor an output an input. */
+ * fewer continuations than n_out the rest gets parent and token -1, score
+ * -infinity, finished 0.  No two of the outputs may overlap, nor an output an
+ * input. */
 gdn_status gdn_beam_select_workspace_bytes(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out,
                                            size_t* bytes);
 gdn_status gdn_beam_select(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype,
@@ -230,7 +230,7 @@ gdn_status gdn_beam_select(int32_t n_req, int32_t width, int32_t vocab, int32_t 
  *                  Rows past max_ckpt are dropped: ckpt_offsets ends there
  * Per-token rows behind the last token are set to -1.  The pool supplies the error
  * word (bits 1 and 2 of gdn_pool_error).  max_tok and every count fit 31 bits, and
- * past + tokens should. */
+ * past + tokens should.  No two of the outputs may overlap, nor an output an input. */
 gdn_status gdn_batch_maps(gdn_pool* pool, int32_t n_seq, const int32_t* lens, int64_t max_tok,
                           int32_t* cu_seqlens, int32_t* last_rows, int32_t* token_seq, const int32_t* past,
                           int32_t* token_pos, const int32_t* adapter_ids, int32_t n_adapters,
@@ -539,9 +539,11 @@ gdn_status gdn_mx_in_proj(const gdn_pool* pool, int64_t n_tok, int32_t hidden, c
  *   rank           a multiple of 8 up to GDN_LORA_MAX_RANK (UNSUPPORTED otherwise;
  *                  smaller ranks are padded with zeros)
  *   workspace      device, >= the workspace bytes, 256-byte aligned; scratch only
- * Without adapters (n_adapters 0) the call is gdn_mx_proj / gdn_mx_in_proj and the
- * adapters' arguments are not looked at.  Infinite adapter weights make the
- * results of their own tokens infinite or NaN. */
+ * The outputs overlap neither each other nor an input.  Without adapters
+ * (n_adapters 0) the call is gdn_mx_proj / gdn_mx_in_proj and the adapters'
+ * arguments are not looked at.  Infinite adapter weights, or a lora_scale x A^T
+ * past bf16's largest value, make the results of their own tokens infinite or
+ * NaN. */
 #define GDN_LORA_MAX_RANK 128
 gdn_status gdn_mx_proj_lora_workspace_bytes(int64_t n_tok, int32_t n_in, int32_t n_out, int32_t rank,
                                             size_t* bytes);

@@ -100,3 +100,50 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         pool.batch_maps(f(0).int(), f(1).int(), token_adapter=f(0).int())
     with pytest.raises(ValueError, match="not a device tensor"):
         pool.batch_maps(f(2).int(), f(3).int())
+
+
+class Elsewhere(torch.Tensor):
+    """Host memory that says it is on a device."""
+    is_cuda = True
+    on = 0
+
+    def get_device(self):
+        return self.on
+
+
+def test_binding_refuses_tensors_of_another_device(monkeypatch):
+    """Every tensor of a call is on the device where the library launches."""
+    import gated_deltanet_state_layer_amd as G
+    from gated_deltanet_state_layer_amd import binding
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+
+    def calls_refuse(call, tensors):
+        for wrong in tensors:
+            args = {}
+            for name, t in tensors.items():
+                args[name] = t.clone().as_subclass(Elsewhere)
+                args[name].on = int(name == wrong)
+            with pytest.raises(ValueError, match=f"{wrong}: on .* but the current device"):
+                call(**args)
+
+    f = torch.zeros
+    i, u, h = torch.int32, torch.uint8, torch.bfloat16
+    calls_refuse(G.mx_proj_lora, dict(
+        x=f(2, 64, dtype=h), codes=f(3, 32, dtype=u), scales=f(3, 2, dtype=u), lora_a=f(1, 8, 64, dtype=h),
+        lora_b=f(1, 3, 8, dtype=h), lora_scale=f(1), token_adapter=f(2, dtype=i), out=f(2, 3), workspace=f(192, dtype=u)))
+    calls_refuse(G.beam_select, dict(
+        logits=f(1, 2, 9), scores=f(1, 2), parents=f(1, 2, dtype=i), tokens=f(1, 2, dtype=i), scores_out=f(1, 2),
+        finished=f(1, 2, dtype=u), finished_out=f(1, 2, dtype=u), workspace=f(999, dtype=u)))
+    pool = G.Pool.__new__(G.Pool)
+    calls_refuse(pool.reorder, dict(slots=f(1, 2, dtype=i), parents=f(1, 2, dtype=i), slots_out=f(1, 2, dtype=i)))
+    pool.desc = type("Desc", (), dict(h_v=1))
+    pool._k_width = pool._v_width = 32
+    pool.c_conv, pool.io_torch = 96, torch.float32
+    calls_refuse(pool.mx_in_proj_lora, dict(
+        x=f(2, 64, dtype=h), codes=f(130, 32, dtype=u), scales=f(130, 2, dtype=u), lora_a=f(1, 8, 64, dtype=h),
+        lora_b=f(1, 130, 8, dtype=h), lora_scale=f(1), token_adapter=f(2, dtype=i), q=f(2, 32), k=f(2, 32),
+        v=f(2, 32), a=f(2, 1), b=f(2, 1), z=f(2, 32), workspace=f(192, dtype=u)))
+    maps = {n: f(4, dtype=i) for n in ("lens", "last_rows", "token_seq", "past", "token_pos", "adapter_ids",
+                                       "token_adapter", "free_slots", "ckpt_slots")}
+    maps.update(cu_seqlens=f(5, dtype=i), ckpt_offsets=f(5, dtype=i))
+    calls_refuse(lambda **k: pool.batch_maps(ckpt_every=2, n_adapters=1, **k), maps)
