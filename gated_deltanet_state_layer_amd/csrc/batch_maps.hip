@@ -1,10 +1,12 @@
 // The maps of a batch from its requests' lengths: starts of the requests, maps
 // from tokens to requests, positions and adapters, and the checkpoint table.
 //
-// A few KB of work: what it costs is the launch and a chain of memory trips, so it
-// is one launch without scratch memory.  Every workgroup loads what the requests
-// bring, scans the lengths itself (4096 at a time, in LDS) and then fills its own
-// rows; no workgroup waits for another.
+// A few KB of work: what it costs is the launch (1.9 us) and a chain of memory
+// trips, so it is one launch without scratch memory.  Every workgroup loads what the
+// requests bring, all loads in one trip, scans the lengths itself (512 to 4096 at a
+// time, in LDS) and then fills its own rows; no workgroup waits for another.  All
+// maps of 64 requests 4.1 us (5.3 with the loads one behind the other and scans
+// through LDS), of 2000 requests with 300001 tokens 6.2 (3.6 MB).
 #include <algorithm>
 
 #include "gdn_common.h"
@@ -72,7 +74,9 @@ __device__ __forceinline__ void put4(int32_t* p, int64_t r, const int (&v)[kRows
         if (in >> i & 1) p[r + i] = v[i];
 }
 
-// PER requests to a thread: as few as hold them all.
+// PER requests to a thread: as few as hold them all, since what the threads scan and
+// put into LDS grows with it (64 requests 4.1 us, eight to a thread 5.4; 2000 requests
+// four to a thread 6.2, eight 6.9).
 template <int PER>
 __global__ __launch_bounds__(kThreads) void batch_maps_kernel(Maps a) {
     constexpr int kChunk = kThreads * PER;

