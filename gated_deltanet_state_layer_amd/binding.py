@@ -355,16 +355,12 @@ def _current_device():
         return -2
 
 
-def _fit(dev, t, numel, dtype):
-    """Whether t is a contiguous tensor of this dtype on device `dev` (the
-    current one, where the library launches) with at least numel elements."""
-    return (t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and
-            t.numel() >= numel)
-
-
 def _want(dev, t, name, numel, dtype):
-    """_fit, or the error that says why not; numel 0 accepts anything."""
-    if numel > 0 and not _fit(dev, t, numel, dtype):
+    """Host-side check of a contiguous tensor of this dtype on device `dev` (the
+    current one, where the library launches) with at least numel elements; numel 0
+    accepts anything."""
+    if numel > 0 and not (t is not None and t.dtype is dtype and t.get_device() == dev and
+                          t.is_contiguous() and t.numel() >= numel):
         _need(t, name, numel, dtype)
         _here(dev, t, name)
 

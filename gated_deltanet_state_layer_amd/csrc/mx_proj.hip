@@ -98,7 +98,7 @@ __device__ __forceinline__ bf16x8 mx_expand(uint32_t c, float scale) {
 // rows of its adapter's B is added to the sums.  MxNoLora: none, and no code for it.
 // In-projections 2048 -> 12352 at rank 16, without adapters and with, of the h before
 // them: 1 token 4.8 and 7.3 us, 64 tokens with one each 13.3 and 22.0 (25 MB of B),
-// 500 tokens with eight in runs 40 and 49, 8192 tokens 476 and 502, 546 with 40.
+// 500 tokens with eight in runs 40 and 49, 8192 tokens 476 and 502 (526 at rank 32).
 struct MxLora {
     const uint16_t* h;   // [n_tok][blocks][3][16]
     const uint16_t* b;   // [n_adapters][n_out][rank]
