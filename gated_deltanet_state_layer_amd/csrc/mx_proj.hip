@@ -97,12 +97,27 @@ __device__ __forceinline__ bf16x8 mx_expand(uint32_t c, float scale) {
 // its adapter, in three bf16 pieces by blocks of 16 ranks: see lora.hip) times the
 // rows of its adapter's B is added to the sums.  MxNoLora: none, and no code for it.
 // In-projections 2048 -> 12352 at rank 16, without adapters and with, of the h before
-// them: 1 token 4.8 and 7.3 us, 64 tokens with one each 13.3 and 22.0 (25 MB of B),
+// them: 1 token 4.5 and 7.3 us, 64 tokens with one each 13.3 and 22.0 (25 MB of B),
 // 500 tokens with eight in runs 40 and 49, 8192 tokens 476 and 502 (526 at rank 32).
 struct MxLora {
     const uint16_t* h;   // [n_tok][blocks][3][16]
     const uint16_t* b;   // [n_adapters][n_out][rank]
     const int32_t* ids;  // [n_tok]
+    int n_adapters, rank, blocks;
+};
+// The same for so little work that every workgroup makes its own h, from A in the L2
+// caches, and the call is one launch.  Two launches and one: 1 x 4096 -> 2048 at rank
+// 16 6.7 and 6.1 us (from Python 11.5 and 8.8), 1 x 2048 -> 12352 7.0 and 7.3 (11.4 and
+// 8.7), 4 x 1024 -> 1024 6.0 and 6.1; past the limit 1 x 4096 -> 2048 at rank 32 7.2
+// and 8.0, 2 x 4096 -> 4096 6.9 and 8.5.
+struct MxLoraHere {
+    static constexpr int kTokens = 4, kBlocks = 2;
+    static bool takes(int64_t n_tok, int n_in, int blocks) {
+        return n_tok <= kTokens && blocks <= kBlocks && n_tok * blocks * n_in <= 4096;
+    }
+    const uint16_t *a, *b;   // [n_adapters][rank][n_in], [n_adapters][n_out][rank]
+    const float* scale;
+    const int32_t* ids;
     int n_adapters, rank, blocks;
 };
 struct MxNoLora {
@@ -118,6 +133,12 @@ __device__ __forceinline__ int lora_ranks(const MxNoLora&) { return 0; }
 
 __device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+__device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fmaf(high_bf16(a[i]), high_bf16(b[i]), fmaf(low_bf16(a[i]), low_bf16(b[i]), s));
+    return s;
+}
 
 // A thread's part of what token t's adapter adds to a tile's 16 NC channels: thread j
 // of the token's TPT takes half the ranks of each 16, and channels i TPT / 2 + j / 2,
@@ -147,6 +168,67 @@ __device__ __forceinline__ void lora_share(const MxLora& l, int64_t t, int n0, i
         }
     }
 }
+
+// h of a workgroup's few tokens and the thread's part of the rows of B (see lora_share).
+struct LoraHere {
+    u32x4 w[MxLoraHere::kBlocks];
+    __device__ __forceinline__ static float* h() {   // [token][rank]
+        __shared__ float v[MxLoraHere::kTokens * MxLoraHere::kBlocks * 16];
+        return v;
+    }
+    __device__ __forceinline__ void load(const MxLoraHere& l, bool in, int t, int row, int n_out, int j) {
+        const int id = in ? l.ids[t] : -1;
+#pragma unroll
+        for (int k = 0; k < MxLoraHere::kBlocks; ++k) {
+            const int r = 16 * k + 8 * (j & 1);
+            w[k] = u32x4{0u, 0u, 0u, 0u};
+            if ((unsigned)id < (unsigned)l.n_adapters && r < l.rank)
+                w[k] = *reinterpret_cast<const u32x4*>(l.b + ((int64_t)id * n_out + row) * l.rank + r);
+        }
+    }
+    // Two ranks of every 16 to a wave.  Two steps at a time: of four at a time, which all
+    // workgroups read at once, 1 x 4096 -> 2048 takes 7.2 us for 6.1.
+    __device__ __forceinline__ void shrink(const MxLoraHere& l, const uint16_t* x, int64_t ld_x, int n_in, int toks,
+                                           int wave) {
+        const int lane = threadIdx.x & 63;
+        for (int i = 0; i < toks * l.blocks; ++i) {
+            const int t = i / l.blocks, r = i % l.blocks * 16 + wave;
+            const int id = l.ids[t];
+            float s0 = 0.f, s1 = 0.f;
+            if ((unsigned)id < (unsigned)l.n_adapters) {
+                // ranks are a multiple of 8: the first of the two is there for every wave or for none
+                const uint16_t* a = l.a + ((int64_t)id * l.rank + r) * n_in;
+                const bool second = r + 8 < l.rank;
+                const uint16_t* a1 = second ? a + 8 * (int64_t)n_in : a;
+#pragma unroll 2
+                for (int c = lane * 8; c < n_in; c += 512) {
+                    const u32x4 v = *reinterpret_cast<const u32x4*>(x + t * ld_x + c);
+                    s0 = dot8(v, *reinterpret_cast<const u32x4*>(a + c), s0);
+                    s1 = dot8(v, *reinterpret_cast<const u32x4*>(a1 + c), s1);
+                }
+                s0 = l.scale[id] * wave_sum(s0);
+                s1 = second ? l.scale[id] * wave_sum(s1) : 0.f;
+            }
+            if (lane == 0) {
+                h()[i * 16 + wave] = s0;
+                h()[i * 16 + wave + 8] = s1;
+            }
+        }
+    }
+    // Behind a barrier.
+    __device__ __forceinline__ float expand(const MxLoraHere& l, int t, int j) const {
+        float y = 0.f;
+#pragma unroll
+        for (int k = 0; k < MxLoraHere::kBlocks; ++k) {
+            if (k >= l.blocks) continue;
+            const float* v = h() + (t * l.blocks + k) * 16 + 8 * (j & 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y = fmaf(high_bf16(w[k][i]), v[2 * i + 1], fmaf(low_bf16(w[k][i]), v[2 * i], y));
+        }
+        return y;
+    }
+};
 
 struct MxIn {
     const uint16_t* x;
@@ -278,13 +360,19 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
     for (int i = 0; i < D; ++i)
         if (s_begin + i < s_end) fetch(s_begin + i, i);
     // The adapters' share, while the first steps arrive: every thread has a token.
-    constexpr bool kLora = std::is_same_v<L, MxLora>;
+    constexpr bool kHere = std::is_same_v<L, MxLoraHere>, kLora = std::is_same_v<L, MxLora> || kHere;
     constexpr int kPerToken = kSkinnyThreads / R, kShare = (32 * NC + kPerToken - 1) / kPerToken;
     const int share_t = threadIdx.x / kPerToken, share_j = threadIdx.x % kPerToken;
     const bool share_in = share_t < toks && share_j < 32 * NC;
     [[maybe_unused]] float share[kShare] = {};
-    if constexpr (kLora)
+    [[maybe_unused]] std::conditional_t<kHere, LoraHere, MxNoLora> here;
+    if constexpr (kHere) {
+        static_assert(R == MxLoraHere::kTokens && kShare == 1, "a thread has half a row of B");
+        here.load(lora, share_in, (int)t0 + share_t, n0 + min(share_j / 2, rows - 1), p.n_out, share_j);
+        here.shrink(lora, p.x, p.ld_x, p.n_in, toks, wave);
+    } else if constexpr (kLora) {
         if (share_in) lora_share<kPerToken>(lora, t0 + share_t, n0, p.n_out, share_j, share);
+    }
 #pragma unroll 1
     for (int st = s_begin; st < s_end; st += D) {
         step(st, 0);
@@ -299,6 +387,7 @@ __global__ __launch_bounds__(kSkinnyThreads, 2) void mx_skinny_kernel(MxIn p, Mx
 #pragma unroll
             for (int c = 0; c < NC; ++c)
                 *reinterpret_cast<f32x4*>(&red[(wave * R + t * 16 + m) * S::LD + c * 16 + 4 * q]) = acc[t][c];
+    if constexpr (kHere) share[0] = here.expand(lora, share_t, share_j);
     if constexpr (kLora) {
 #pragma unroll
         for (int i = 0; i < kShare; ++i) {
@@ -748,7 +837,7 @@ bool fits(const void* p, int64_t ld, int elem, int vec) {
 
 template <typename T, int R, int NC, int D = 2, typename L>
 hipError_t skinny(const MxIn& p, const MxOut& o, const MxLaunch& l, const L& lora, hipStream_t stream) {
-    constexpr int lds = std::is_same_v<L, MxLora> ? SkinnyShape<R, NC, D>::kLoraBytes : SkinnyShape<R, NC, D>::kBytes;
+    constexpr int lds = std::is_same_v<L, MxNoLora> ? SkinnyShape<R, NC, D>::kBytes : SkinnyShape<R, NC, D>::kLoraBytes;
     static_assert(lds <= 160 * 1024, "fits");
     if (lds > 65536) {
         static std::atomic<uint64_t> done{0};
@@ -803,11 +892,27 @@ hipError_t launch_any(gdn_dtype out, const MxIn& p, const MxOut& o, const L& lor
     return out == GDN_BF16 ? launch_typed<uint16_t>(p, o, lora, stream) : launch_typed<float>(p, o, lora, stream);
 }
 
+template <typename T>
+hipError_t launch_here(const MxIn& p, const MxOut& o, const MxLaunch& m, const MxLoraHere& lora, hipStream_t stream) {
+    return m.channels == 16 ? skinny<T, 4, 1>(p, o, m, lora, stream) : skinny<T, 4, 2>(p, o, m, lora, stream);
+}
+
 hipError_t launch_with(gdn_dtype out, const MxIn& p, const MxOut& o, const LoraArgs& l, hipStream_t stream) {
+    const int blocks = (l.rank + 15) / 16;
+    if (MxLoraHere::takes(p.n_tok, p.n_in, blocks)) {
+        const MxPlan plan = mx_plan(p.n_tok, p.n_in, p.n_out);
+        const MxLaunch& m = plan.launch[0];
+        if (plan.n == 1 && !m.tile && m.tokens == 4 && (m.channels == 16 || m.channels == 32)) {
+            const MxLoraHere lora{static_cast<const uint16_t*>(l.a), static_cast<const uint16_t*>(l.b), l.scale, l.ids,
+                                  l.n_adapters, l.rank, blocks};
+            return out == GDN_BF16 ? launch_here<uint16_t>(p, o, m, lora, stream)
+                                   : launch_here<float>(p, o, m, lora, stream);
+        }
+    }
     const hipError_t e = launch_lora_shrink(p.n_tok, p.n_in, p.x, p.ld_x, l, stream);
     if (e != hipSuccess) return e;
     const MxLora lora{static_cast<const uint16_t*>(l.h), static_cast<const uint16_t*>(l.b), l.ids,
-                      l.n_adapters, l.rank, (l.rank + 15) / 16};
+                      l.n_adapters, l.rank, blocks};
     return launch_any(out, p, o, lora, stream);
 }
 

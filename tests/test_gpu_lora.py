@@ -115,6 +115,18 @@ def test_proj(G, n_tok, n_in, n_out, rank, n, out, kind):
     _case(G, n_tok, n_in, n_out, rank, n, kind, out)
 
 
+@pytest.mark.parametrize("kind", ["one", "each", "mixed"])
+@pytest.mark.parametrize("n_tok,n_in,n_out,rank", [
+    (1, 4096, 8200, 16), (1, 4096, 47, 8), (1, 4128, 47, 16), (1, 2048, 4113, 32), (1, 2048, 1000, 24), (1, 2080, 99, 24),
+    (1, 128, 16, 32), (1, 544, 33, 40), (2, 2048, 515, 16), (2, 1024, 8193, 32), (3, 1344, 100, 8), (3, 672, 515, 24),
+    (4, 1024, 4100, 16), (4, 1056, 65, 16), (4, 512, 272, 32), (4, 128, 1, 8), (5, 128, 48, 16),
+])
+def test_proj_of_few_tokens(G, n_tok, n_in, n_out, rank, kind):
+    """Both sides of what one launch takes."""
+    _case(G, n_tok, n_in, n_out, rank, 4, kind, BF, pad_x=8)
+    _case(G, n_tok, n_in, n_out, rank, 4, kind, F32)
+
+
 @pytest.mark.parametrize("kind", ["runs", "mixed"])
 @pytest.mark.parametrize("n_tok,n_in,n_out,want", TILE_CASES)
 def test_proj_on_tiles(G, n_tok, n_in, n_out, want, kind):
