@@ -30,8 +30,8 @@ inline MxLaunch mx_launch(bool tile, int64_t n_tok, int tokens, int channels, in
     return {tile, tokens, channels, c0, c1, mx_tiles(n_tok, c1 - c0, tokens, channels)};
 }
 
-// The calls that are taken: 32 tokens by 64 channels, the largest skinny shape,
-// are then fewer than 2^23 workgroups.
+// The calls that are taken: 32 tokens by 64 channels, the skinny shape that a strip
+// has, are then fewer than 2^23 workgroups.
 inline bool mx_proj_fits(int64_t n_tok, int64_t n_out) {
     const int64_t t = n_tok / 64 + 1, c = n_out / 64 + 1;
     return t < (1 << 22) && t * c < (1 << 22);
@@ -42,7 +42,9 @@ inline bool mx_proj_fits(int64_t n_tok, int64_t n_out) {
 // per 1024 inputs; of tiles about 4 us and, per 1024 inputs, 8.8 (128x128) or
 // 12.2 (128x192).  Fitted to 19 token counts of 24 to 8192 for each of eleven
 // pairs of 128 to 8192 inputs and 1001 to 16384 channels: what is picked takes
-// 0.5 % longer than the fastest way on average, 17 % at worst.
+// 0.5 % longer than the fastest of these on average, 17 % at worst.  The 64-token
+// shape is no part of it: tiles add in another order, and a call keeps its bits
+// (128 x 2048 -> 12352 takes tiles, 26.6 us, and would take 18.7 in that shape).
 inline int64_t mx_skinny_time(int64_t n_tok, int32_t n_in, int64_t n_out) {
     return mx_rounds(mx_tiles(n_tok, n_out, 32, 64)) * (2560 + (int64_t)n_in * 8 / 5);
 }
@@ -75,10 +77,12 @@ inline MxTiles mx_plan_tiles(int64_t n_tok, int32_t n_in, int64_t n_out) {
 
 // The skinny kernel's shape for a call of its own: by the bytes that the busiest
 // CU takes in, the tile's tokens and weights, the measure that separates the
-// shapes where the axis is not the limit.
+// shapes where the axis is not the limit.  64 tokens where that saves a round or
+// two: 64 x 2048 -> 12352 13.1 -> 9.8 us, 300 x 2048 -> 2048 12.4 -> 8.8, 1000 x 1056
+// -> 1001 11.5 -> 9.9; the same bits, as every shape adds in one order.
 inline MxLaunch mx_plan_skinny(int64_t n_tok, int64_t n_out) {
-    constexpr int shapes[][2] = {{4, 16}, {4, 32}, {16, 16}, {16, 32}, {16, 64}, {32, 64}};
-    const int first = n_tok <= 4 ? 0 : 2, last = n_tok <= 4 ? 2 : 6;
+    constexpr int shapes[][2] = {{4, 16}, {4, 32}, {16, 16}, {16, 32}, {16, 64}, {32, 64}, {64, 64}};
+    const int first = n_tok <= 4 ? 0 : 2, last = n_tok <= 4 ? 2 : 7;
     int best = first;
     int64_t least = INT64_MAX;
     for (int i = first; i < last; ++i) {

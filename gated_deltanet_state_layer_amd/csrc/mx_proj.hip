@@ -97,7 +97,7 @@ __device__ __forceinline__ bf16x8 mx_expand(uint32_t c, float scale) {
 // its adapter, in three bf16 pieces by blocks of 16 ranks: see lora.hip) times the
 // rows of its adapter's B is added to the sums.  MxNoLora: none, and no code for it.
 // In-projections 2048 -> 12352 at rank 16, without adapters and with, of the h before
-// them: 1 token 4.5 and 7.3 us, 64 tokens with one each 13.3 and 22.0 (25 MB of B),
+// them: 1 token 4.5 and 7.3 us, 64 tokens with one each 9.8 and 17.6 (25 MB of B),
 // 500 tokens with eight in runs 40 and 49, 8192 tokens 476 and 502 (526 at rank 32).
 struct MxLora {
     const uint16_t* h;   // [n_tok][blocks][3][16]
@@ -254,7 +254,7 @@ struct MxIn {
 // step come as one word).  One token 2048 -> 12352 5.7 us (13.4 MB of weights at
 // 5.0 TB/s would take 2.7, a launch takes 1.9), 64 tokens 4096 -> 2048 5.9 us;
 // operand-order loads 7.7 and 9.8.  D = 1 where two steps do not fit: 32 tokens
-// by 64 channels of LDS would be 192 KiB.
+// by 64 channels of LDS would be 192 KiB; 64 by 64 take all 160 with one.
 constexpr int kSkinnyThreads = kMxWorkgroup, kSkinnyWaves = kSkinnyThreads / 64;
 
 template <int R, int NC, int D>
@@ -873,6 +873,7 @@ hipError_t launch_one(const MxIn& p, const MxOut& o, const MxLaunch& l, const L&
         case 16 * 256 + 32: return skinny<T, 16, 2>(p, o, l, lora, stream);
         case 16 * 256 + 64: return skinny<T, 16, 4>(p, o, l, lora, stream);
         case 32 * 256 + 64: return skinny<T, 32, 4, 1>(p, o, l, lora, stream);
+        case 64 * 256 + 64: return skinny<T, 64, 4, 1>(p, o, l, lora, stream);
         default: return hipErrorInvalidValue;   // a shape without a kernel
     }
 }

@@ -2,7 +2,7 @@
 their definition in float64."""
 import pytest
 
-from mx_plan import TILE_CASES, paths
+from mx_plan import TILE_CASES, paths, plan
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -125,6 +125,22 @@ def test_proj_of_few_tokens(G, n_tok, n_in, n_out, rank, kind):
     """Both sides of what one launch takes."""
     _case(G, n_tok, n_in, n_out, rank, 4, kind, BF, pad_x=8)
     _case(G, n_tok, n_in, n_out, rank, 4, kind, F32)
+
+
+@pytest.mark.parametrize("kind", ["each", "mixed"])
+@pytest.mark.parametrize("n_tok,n_in,n_out,rank", [
+    (64, 2048, 12352, 16), (33, 1056, 12301, 24), (64, 1056, 16370, 8), (700, 544, 1001, 16), (999, 1184, 515, 40),
+    (300, 2048, 2048, 16), (193, 1056, 4090, 128), (97, 1056, 8180, 16), (255, 1056, 4080, 8),
+])
+def test_proj_in_shapes_of_64_tokens(G, n_tok, n_in, n_out, rank, kind):
+    """And tokens without an adapter have the plain projection's bits."""
+    assert [(p.tile, p.tokens) for p in plan(n_tok, n_in, n_out)] == [(0, 64)]
+    x, codes, scales, _, _, _, ids, y = _case(G, n_tok, n_in, n_out, rank, 9, kind, BF, pad_x=8)
+    plain = torch.empty_like(y)
+    G.mx_proj(x, codes, scales, plain)
+    off = (ids < 0) | (ids >= 9)
+    assert torch.equal(y[off], plain[off])
+    _case(G, n_tok, n_in, n_out, rank, 9, kind, F32)
 
 
 @pytest.mark.parametrize("kind", ["runs", "mixed"])
