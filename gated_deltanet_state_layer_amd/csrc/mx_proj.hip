@@ -97,7 +97,7 @@ __device__ __forceinline__ bf16x8 mx_expand(uint32_t c, float scale) {
 // its adapter, in three bf16 pieces by blocks of 16 ranks: see lora.hip) times the
 // rows of its adapter's B is added to the sums.  MxNoLora: none, and no code for it.
 // In-projections 2048 -> 12352 at rank 16, without adapters and with, of the h before
-// them: 1 token 4.5 and 7.3 us, 64 tokens with one each 9.8 and 17.6 (25 MB of B),
+// them: 1 token 4.5 and 7.3 us, 64 tokens with one each 9.8 and 16.7 (25 MB of B),
 // 500 tokens with eight in runs 40 and 49, 8192 tokens 476 and 502 (526 at rank 32).
 struct MxLora {
     const uint16_t* h;   // [n_tok][blocks][3][16]
@@ -142,7 +142,50 @@ __device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float s) {
 
 // A thread's part of what token t's adapter adds to a tile's 16 NC channels: thread j
 // of the token's TPT takes half the ranks of each 16, and channels i TPT / 2 + j / 2,
-// so that neighbouring lanes read B side by side.
+// so that neighbouring lanes read B side by side.  G blocks of 16 ranks at a time, of
+// 16 / G channels: a row's 32 G bytes are one thread's loads behind each other, and
+// come as one line (64 tokens with an adapter each, 2048 -> 12352: at rank 64 45 us for
+// 66 with 16 ranks of all channels first, 32 tokens 21 for 32).
+template <int TPT, int E, int G>
+__device__ __forceinline__ void lora_share(const MxLora& l, const uint16_t* h, const uint16_t* b, int ranks, int j,
+                                           int last, float (&y)[E]) {
+    constexpr int C = E < 16 / G ? E : 16 / G;
+    static_assert(E % C == 0, "whole groups of channels");
+    float v[G][8];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        u32x4 p[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            p[i] = 16 * g < ranks ? *reinterpret_cast<const u32x4*>(h + 48 * g + 16 * i) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {   // the pieces' sum is exact
+            v[g][2 * k] = low_bf16(p[0][k]) + (low_bf16(p[1][k]) + low_bf16(p[2][k]));
+            v[g][2 * k + 1] = high_bf16(p[0][k]) + (high_bf16(p[1][k]) + high_bf16(p[2][k]));
+        }
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < E; i0 += C) {
+        u32x4 w[C][G];
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                w[i][g] = 16 * g < ranks ? *reinterpret_cast<const u32x4*>(
+                                               b + min((i0 + i) * (TPT / 2) + j / 2, last) * l.rank + 16 * g)
+                                         : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < C; ++i)
+                    y[i0 + i] = fmaf(high_bf16(w[i][g][k]), v[g][2 * k + 1],
+                                     fmaf(low_bf16(w[i][g][k]), v[g][2 * k], y[i0 + i]));
+        __builtin_amdgcn_sched_barrier(0);   // one group's loads in registers at a time
+    }
+}
+
 template <int TPT, int E>
 __device__ __forceinline__ void lora_share(const MxLora& l, int64_t t, int n0, int n_out, int j, float (&y)[E]) {
     const int id = l.ids[t];
@@ -150,22 +193,15 @@ __device__ __forceinline__ void lora_share(const MxLora& l, int64_t t, int n0, i
     const int r0 = 8 * (j & 1), last = n_out - 1 - n0;   // rows past the end repeat the last one
     const uint16_t* b = l.b + ((int64_t)id * n_out + n0) * l.rank + r0;
     const uint16_t* h = l.h + t * l.blocks * 48 + r0;
+    constexpr int kMost = E > 8 ? 2 : 4;   // four of 16 channels each spill
+    if (l.blocks == 1) {
+        lora_share<TPT, E, 1>(l, h, b, l.rank - r0, j, last, y);
+    } else if (l.blocks == 2) {
+        lora_share<TPT, E, 2>(l, h, b, l.rank - r0, j, last, y);
+    } else {
 #pragma unroll 1
-    for (int r = 0; r + r0 < l.rank; r += 16, h += 48) {
-        u32x4 w[E], p[3];
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            w[i] = *reinterpret_cast<const u32x4*>(b + min(i * (TPT / 2) + j / 2, last) * l.rank + r);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) p[i] = *reinterpret_cast<const u32x4*>(h + 16 * i);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            // the pieces' sum is exact
-            const float h0 = low_bf16(p[0][k]) + (low_bf16(p[1][k]) + low_bf16(p[2][k]));
-            const float h1 = high_bf16(p[0][k]) + (high_bf16(p[1][k]) + high_bf16(p[2][k]));
-#pragma unroll
-            for (int i = 0; i < E; ++i) y[i] = fmaf(high_bf16(w[i][k]), h1, fmaf(low_bf16(w[i][k]), h0, y[i]));
-        }
+        for (int r = 0; r < l.rank; r += 16 * kMost)
+            lora_share<TPT, E, kMost>(l, h + 3 * r, b + r, l.rank - r0 - r, j, last, y);
     }
 }
 
