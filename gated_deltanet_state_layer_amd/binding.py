@@ -365,6 +365,17 @@ def _want(dev, t, name, numel, dtype):
         _here(dev, t, name)
 
 
+def _shaped(dev, t, name, shape, dtype):
+    """_want of a matrix of this shape."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
+    if t is None:
+        raise ValueError(f"{name}: missing")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    _want(dev, t, name, shape[0] * shape[1], dtype)
+
+
 def _here(dev, t, name):
     """A tensor that is not on device `dev` is an error."""
     if t.get_device() != dev and t.numel() > 0:
@@ -375,9 +386,10 @@ def _workspace(dev, ws):
     """A workspace's pointer and bytes."""
     if ws is None:
         return None, 0
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("workspace: not a contiguous device tensor")
-    _here(dev, ws, "workspace")
+    if ws.get_device() != dev or not ws.is_contiguous():
+        if not ws.is_cuda or not ws.is_contiguous():
+            raise ValueError("workspace: not a contiguous device tensor")
+        _here(dev, ws, "workspace")
     return ws.data_ptr(), ws.nbytes
 
 
@@ -459,17 +471,14 @@ def beam_select(logits, scores, parents, tokens, scores_out, finished=None, fini
         _need(logits, "logits", max(1, logits.numel()), logits.dtype)
         _here(dev, logits, "logits")
     wide, kept = (n_req, width), (n_req, n_out)
-    for t, name, shape, dt in ((scores, "scores", wide, torch.float32), (parents, "parents", kept, torch.int32),
-                               (tokens, "tokens", kept, torch.int32), (scores_out, "scores_out", kept, torch.float32),
-                               (finished, "finished", wide, torch.uint8),
-                               (finished_out, "finished_out", kept, torch.uint8)):
-        if t is None:
-            if name.startswith("finished"):
-                continue
-            raise ValueError(f"{name}: missing")
-        if t.shape != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-        _want(dev, t, name, shape[0] * shape[1], dt)
+    _shaped(dev, scores, "scores", wide, torch.float32)
+    _shaped(dev, parents, "parents", kept, torch.int32)
+    _shaped(dev, tokens, "tokens", kept, torch.int32)
+    _shaped(dev, scores_out, "scores_out", kept, torch.float32)
+    if finished is not None:
+        _shaped(dev, finished, "finished", wide, torch.uint8)
+    if finished_out is not None:
+        _shaped(dev, finished_out, "finished_out", kept, torch.uint8)
     ws, ws_bytes = _workspace(dev, workspace)
     _check(lib.gdn_beam_select(n_req, width, vocab, n_out, code, logits.data_ptr(), ld,
                                scores.data_ptr(), _ptr(finished), eos, parents.data_ptr(),
