@@ -14,7 +14,7 @@
 // units run them at fp32's rate.
 //
 // What bounds it is issuing these instructions, not memory: 64 x 8 x 131072 bf16
-// (134 MB) take 60 us (2.2 TB/s), 45 without exponentials, 37 without the selection,
+// (134 MB) take 59 us (2.3 TB/s), 45 without exponentials, 37 without the selection,
 // about as much when the logits lie in the L2 caches.  In fp32 (268 MB) 76 us, 3.5
 // TB/s.  1 x 4 x 32000: 9.3 us, of which two launches are 3.8.
 #include <algorithm>
@@ -260,12 +260,14 @@ struct ExpTable {
     static constexpr int kBytes = 2 * kSize * 8;
     static_assert(kBytes < 65536, "byte offsets in 16 bits");
     static __device__ __forceinline__ void fill(double* t, int thread, int threads) {
-        for (int i = thread; i < 2 * kSize; i += threads) {
-            const int j = i % kSize;
+        for (int j = thread; j < kSize; j += threads) {
             const double x = (double)bf16_to_f32((uint16_t)(kFirst - 1 + j));
-            // exp64 takes what is not above 0
-            const double down = exp64(-x);
-            t[i] = j == 0 ? 1.0 : j == kSize - 1 ? 0.0 : i < kSize ? 1.0 / down : down;
+            const double up = fma(x, kLog2e, kMagic), down = kMagic - (up - kMagic), rest = fma(up - kMagic, -kLn2, x);
+            const double m[2] = {up, down}, r[2] = {rest, -rest};   // exp(x) and exp(-x)
+            double e[2];
+            exp_scaled(r, m, e);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) t[i * kSize + j] = j == 0 ? 1.0 : j == kSize - 1 ? 0.0 : e[i];
         }
     }
     // Byte offsets of two values; the smaller of their places (0: below 2^-13).
@@ -579,9 +581,9 @@ Shape beam_shape(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, int
 
 // Workgroups of eight waves with the table, two to a CU, where each has eight steps or
 // more to fill it for; of four waves otherwise, four to a CU.  With the table and
-// without it: 64 x 8 x 131072 60 and 73 us, 32 x 8 x 131072 40 and 44, 64 x 8 x 32000
-// (eight steps) 30.3 and 30.9, 64 x 4 x 32000 (four) 22.7 and 20.4, 1 x 4 x 32000 12.7
-// and 9.6.  Twice the workgroups with the table: 77 us for 64 x 8 x 131072.
+// without it: 64 x 8 x 131072 59 and 73 us, 32 x 8 x 131072 38 and 44, 64 x 8 x 32000
+// (eight steps) 28.7 and 30.9, 64 x 4 x 32000 (four) 21.0 and 20.2, 1 x 4 x 32000 12.7
+// and 9.5.  Twice the workgroups with the table: 77 us for 64 x 8 x 131072.
 Shape beam_plan(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype) {
     const Shape s = beam_shape(n_req, width, vocab, n_out, 8, 512);
     return dtype == GDN_BF16 && s.steps >= 8 ? s : beam_shape(n_req, width, vocab, n_out, 4, 1024);
