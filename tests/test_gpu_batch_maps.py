@@ -167,3 +167,15 @@ def test_the_maps_feed_a_prefill_with_checkpoints(G):
         b.prefill(0, i32([0, 32]), i32([slot]), 32, chunk, q[s], k[s], v[s], ga[s], gb[s], w, o2, workspace=ws)
     assert torch.equal(a.state, b.state) and torch.equal(a.window, b.window)
     assert a.error() == 0 and b.error() == 0
+
+
+def test_more_tokens_than_2_30(G, pool):
+    a, b, room = 600_000_001, 600_000_006, 1_200_000_100
+    lens = torch.tensor([a, 0, b], dtype=torch.int32, device="cuda")
+    seq = torch.full((room + 1,), GUARD, dtype=torch.int32, device="cuda")
+    cu = torch.empty(4, dtype=torch.int32, device="cuda")
+    pool.batch_maps(lens, cu, token_seq=seq[:room])
+    torch.cuda.synchronize()
+    assert cu.tolist() == [0, a, a, a + b]
+    assert (seq[:a] == 0).all() and (seq[a:a + b] == 2).all() and (seq[a + b:room] == -1).all() and int(seq[room]) == GUARD
+    assert pool.error() == 0

@@ -187,3 +187,41 @@ def test_captured_beam_steps_equal_eager_ones(E, n, w):
             assert torch.equal(getattr(a, name), getattr(b, name)), (t, name)
     assert torch.equal(a.stack.pool.state, b.stack.pool.state) and torch.equal(a.stack.pool.window, b.stack.pool.window)
     assert a.stack.pool.error() == 0 and bool(torch.isfinite(a.scores).all())
+
+
+def test_two_graphs_share_a_workspace():
+    """A projection with adapters in one graph, a selection in another, both with
+    the same scratch memory, replayed in turn."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import gated_deltanet_state_layer_amd as G
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    t, n_in, n_out, rank, r, w, v, k = 300, 512, 700, 24, 4, 5, 30011, 8
+    x, y, want = (rnd(t, c).to(torch.bfloat16) for c in (n_in, n_out, n_out))
+    codes = torch.randint(0, 256, (n_out, n_in // 2), generator=gen, device="cuda").to(torch.uint8)
+    scales = torch.randint(118, 124, (n_out, n_in // 32), generator=gen, device="cuda").to(torch.uint8)
+    a, b, s = rnd(3, rank, n_in).to(torch.bfloat16), rnd(3, n_out, rank).to(torch.bfloat16), rnd(3)
+    ids = (torch.arange(t, device="cuda") % 4).int()
+    logits, scores = rnd(r, w, v), -torch.rand(r, w, generator=gen, device="cuda")
+    outs, expect = ([torch.empty(r, k, dtype=d, device="cuda") for d in (torch.int32, torch.int32, torch.float32)]
+                    for _ in "ab")
+    size = max(G.mx_proj_lora_workspace_bytes(t, n_in, n_out, rank), G.beam_select_workspace_bytes(r, w, v, k))
+    ws, own = (torch.empty(size, dtype=torch.uint8, device="cuda") for _ in "ab")
+    proj, select, side = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(proj, stream=side):
+        G.mx_proj_lora(x, codes, scales, a, b, s, ids, y, workspace=ws)
+    with torch.cuda.graph(select, stream=side):
+        G.beam_select(logits, scores, *outs, workspace=ws)
+    for step in range(5):
+        x.copy_(rnd(t, n_in))
+        logits.copy_(rnd(r, w, v))
+        for graph in (proj, select) if step % 2 else (select, proj):
+            graph.replay()
+        G.mx_proj_lora(x, codes, scales, a, b, s, ids, want, workspace=own)
+        G.beam_select(logits, scores, *expect, workspace=own)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), step
+        for got, ref in zip(outs, expect):
+            assert torch.equal(got, ref), step

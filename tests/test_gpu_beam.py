@@ -256,3 +256,23 @@ def test_repeats_on_another_stream_and_in_a_graph(G):
         torch.cuda.synchronize()
         for a, b in zip(outs, eager):
             assert torch.equal(a, b), t
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_far_apart(G, dtype):
+    """Two rows more than 2^31 elements from each other."""
+    v, k, ld = 50001, 9, 2 ** 31 + 17
+    buf = torch.empty(ld + v, dtype=dtype, device="cuda")
+    x = buf.as_strided((2, 1, v), (ld, ld, 1))
+    near = _logits(_gen(10), 2, 1, v, dtype).cuda()
+    x.copy_(near)
+    scores = torch.zeros(2, 1, device="cuda")
+    ws = torch.empty(G.beam_select_workspace_bytes(2, 1, v, k), dtype=torch.uint8, device="cuda")
+    got = []
+    for logits in (x, near):
+        outs = [torch.empty(2, k, dtype=d, device="cuda") for d in (torch.int32, torch.int32, F32)]
+        G.beam_select(logits, scores, *outs, workspace=ws)
+        got.append(outs)
+    torch.cuda.synchronize()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)

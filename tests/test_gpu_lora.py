@@ -297,3 +297,23 @@ def test_refusals(G):
         G.mx_proj_lora(*good[:3], t(2, 12, 64), t(2, 10, 12), *good[5:], workspace=ws)
     with pytest.raises(ValueError):
         G.mx_proj_lora(*good, workspace=ws.cpu())
+
+
+@pytest.mark.parametrize("n_tok", [1, 40, 300])
+@pytest.mark.parametrize("n_in,n_out,n,rank", [(128, 12352, 6000, 32), (16384, 48, 4200, 32)])
+def test_adapters_past_2_31_elements(G, n_in, n_out, n, rank, n_tok):
+    """The last of many adapters gives what it gives alone."""
+    assert n * rank * max(n_in, n_out) > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(n_tok, n_in, generator=gen, device="cuda").to(BF)
+    codes, scales = _weights(n_out, n_in, gen)
+    a1, b1, s1 = _adapters(1, rank, n_in, n_out, gen)
+    a, b, s = (torch.zeros(n, *t.shape[1:], dtype=t.dtype, device="cuda") for t in (a1, b1, s1))
+    a[-1], b[-1], s[-1] = a1[0], b1[0], s1[0]
+    y, alone = (torch.empty(n_tok, n_out, dtype=BF, device="cuda") for _ in "ab")
+    ws = _ws(G.mx_proj_lora_workspace_bytes(n_tok, n_in, n_out, rank))
+    ids = torch.full((n_tok,), n - 1, dtype=torch.int32, device="cuda")
+    G.mx_proj_lora(x, codes, scales, a, b, s, ids, y, workspace=ws)
+    G.mx_proj_lora(x, codes, scales, a1, b1, s1, torch.zeros_like(ids), alone, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(y, alone)

@@ -132,3 +132,19 @@ def test_graph_replays_in_place(G):
         assert torch.equal(slots, other), t
         for x, y in zip(_parts(pool), _parts(twin)):
             assert torch.equal(x, y), t
+
+
+def test_slots_past_4_gib(G):
+    """Copies among the last slots of a pool of 2^32 state bytes and more."""
+    pool = G.Pool(G.make_desc(2100, 1, 16, 32, 128, 128, 4))
+    assert pool.state.numel() * 4 > 2 ** 32
+    for slot in (2, 2098, 2099):
+        pool.state[slot] = slot
+        pool.window[slot] = slot
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    slots = i32([[2099, 2, 2098]])
+    pool.reorder(slots, i32([[0, 0, 1]]), slots)
+    torch.cuda.synchronize()
+    assert slots.tolist() == [[2099, 2098, 2]]
+    for slot, held in ((2, 2), (2098, 2099), (2099, 2099)):
+        assert (pool.state[slot] == held).all() and (pool.window[slot] == pool.window[held]).all()
