@@ -174,9 +174,10 @@ hipError_t launch_lora_shrink(int64_t n_tok, int32_t n_in, const void* x, int64_
                               hipStream_t stream) {
     const int blocks = (l.rank + 15) / 16;
     const uint16_t* xp = static_cast<const uint16_t*>(x);
-    // Rows up to here: before projections of 16 tokens at rank 16 10.0 us in all for
-    // 11.9 with the tiles, of 64 2 us less, of 500 tokens either way 53; beyond, of 1500
-    // tokens (one adapter) 112 for 108, of 500 at rank 64 58.5 for 52.9.
+    // Rows up to here, which do not mind how many adapters there are.  Tiles and rows, with
+    // a projection 2048 -> 256 behind them at rank 16: 64 tokens 8.2 and 6.9 us; 500 tokens
+    // 9.3 and 9.8 with four adapters in turn, 11.9 and 9.8 with 64; 1000 tokens at rank 32
+    // 13.1 and 19.2 with four.
     if (n_tok * blocks <= 768) {
         hipLaunchKernelGGL(lora_rows_kernel, dim3((unsigned)(n_tok * blocks * 16 / kWaves)), dim3(kThreads), 0, stream,
                            l, xp, ld_x, n_in, blocks);
