@@ -7,7 +7,9 @@
 // exp(x - c), c a logit near the largest so far, and compare each element with the
 // last key that counts, a key being logit and token.  The few that pass wait in
 // LDS; once there are 64, one wave sorts them, one to a lane, and merges them into
-// the sorted list of the best 64.
+// the sorted list of the best 64.  In the end each sum is divided by the term of the
+// stretch's largest logit, made in the same way: a row that is all but certain of a
+// token has a sum of 1 and little more, and of 1 exactly with one token left.
 //
 // Scores of different beams may lie closer than 32 bits resolve, and tokens are
 // whole numbers, right or wrong.  So exponentials and sums are fp64 here: the vector
@@ -41,17 +43,20 @@ constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453;
 constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: a sum's low bits are its integer
 
 // exp(r) 2^n of N values side by side, |r| <= ln 2 / 2 or a little more, n in the low
-// bits of m.  The polynomial is the Chebyshev interpolation of degree 8 (1.1e-12).
+// bits of m.  The polynomial is 1 + r + r^2 q(r), q the Chebyshev interpolation of
+// degree 8 (1.2e-15, what fp64 rounds), so that exp(0) is 1.  Degrees 8 and 9 in all
+// leave 2e-12 and 7e-14, where scores below 1 are told apart by 2^-40 of themselves.
 // The barriers keep the N chains of dependent products interleaved.
 template <int N>
 __device__ __forceinline__ void exp_scaled(const double (&r)[N], const double (&m)[N], double (&p)[N]) {
-    constexpr double kCoef[] = {2.4876070919998397e-05, 0.00019915868674658883, 0.001388882190450549,
-                                0.008333266094398913,   0.04166666688931224,    0.16666666891065027,
-                                0.4999999999980122,     0.9999999999797838,     1.0000000000000004};
+    constexpr double kCoef[] = {2.761379764561564e-07, 2.7625104515531025e-06, 2.4801536405296596e-05,
+                                0.0001984120875246986, 0.001388888890587323,   0.00833333335371942,
+                                0.041666666666651364,  0.166666666666483,      0.5, 1.0, 1.0};
+    constexpr int kTerms = sizeof(kCoef) / sizeof(double);
 #pragma unroll
     for (int k = 0; k < N; ++k) p[k] = kCoef[0];
 #pragma unroll
-    for (int j = 1; j < 9; ++j) {
+    for (int j = 1; j < kTerms; ++j) {
 #pragma unroll
         for (int k = 0; k < N; ++k) p[k] = fma(p[k], r[k], kCoef[j]);
         if constexpr (N > 1) __builtin_amdgcn_sched_barrier(0);
@@ -224,7 +229,8 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// What a stretch of a row leaves: the sum of exp(x - c), beside its best keys.
+// What a stretch of a row leaves: its largest logit c and the sum of exp(x - c), beside
+// its best keys.
 struct Stretch {
     double c, sum;
 };
@@ -270,7 +276,9 @@ struct ExpTable {
             for (int i = 0; i < 2; ++i) t[i * kSize + j] = j == 0 ? 1.0 : j == kSize - 1 ? 0.0 : e[i];
         }
     }
-    // Byte offsets of two values; the smaller of their places (0: below 2^-13).
+    // exp(d) - 1 of magnitudes below 2^-13, beside the entry of 1.
+    static __device__ __forceinline__ double rest(double d) { return fma(d * d, fma(d, 1.0 / 6.0, 0.5), d); }
+    // Byte offsets of two values; their places (0: below 2^-13).
     static __device__ __forceinline__ u16x2 offsets(uint32_t two, u16x2& place) {
         const u16x2 b = __builtin_bit_cast(u16x2, two), size = {kSize * 8, kSize * 8}, lo = {kFirst - 1, kFirst - 1};
         const u16x2 m = __builtin_elementwise_max(__builtin_bit_cast(u16x2, two & 0x7fff7fffu), lo) - lo;
@@ -290,7 +298,7 @@ __global__ __launch_bounds__(64 * W) void beam_rows_kernel(Shape sh, const T* lo
     [[maybe_unused]] auto* table = reinterpret_cast<double*>(lds + sizeof(u32x2) * kHeld * kWaves);
     __shared__ uint64_t list[64], lists[kWaves / 2][64];
     __shared__ int kept[2][kWaves];   // of even and odd steps: the last step's may still be read
-    __shared__ double sums[kWaves], tops[kWaves];
+    __shared__ double sums[kWaves];
     __shared__ float2 bounds[kWaves];
     __shared__ float last;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -306,7 +314,8 @@ __global__ __launch_bounds__(64 * W) void beam_rows_kernel(Shape sh, const T* lo
     const int alone = 64 >> (sh.n_out > 1 ? 32 - __builtin_clz(sh.n_out - 1) : 0);
     const int group = min(64, alone * kWaves);
     // Sums are of exp(x - c) with c = n ln 2, so that the exponent's integer takes c in;
-    // where |c| is large, x is first made x - base in fp32, exact where it counts.
+    // where |c| is large, x is first made x - base in fp32, exact where it counts.  That
+    // c is no logit, so the largest one's term is 1 within its rounding only.
     float c = -FLT_MAX, base = c, least = kNone;   // least: the list's last key that counts
     double shift = kMagic, sum = 0.0;
     [[maybe_unused]] bool by_table = false;   // the wave's largest is -20 to 64 so far, and c is 0
@@ -391,10 +400,7 @@ __global__ __launch_bounds__(64 * W) void beam_rows_kernel(Shape sh, const T* lo
                 for (int k = 0; k < kPer; ++k) sum += e[k];
                 if (__any(least_place[0] == 0 || least_place[1] == 0)) {
 #pragma unroll
-                    for (int k = 0; k < kPer; ++k) {   // exp(x) - 1 of magnitudes below 2^-13
-                        const double d = fabsf(x[k]) < 0x1p-13f ? (double)x[k] : 0.0;
-                        sum += fma(d * d, fma(d, 1.0 / 6.0, 0.5), d);
-                    }
+                    for (int k = 0; k < kPer; ++k) sum += ExpTable::rest(fabsf(x[k]) < 0x1p-13f ? (double)x[k] : 0.0);
                 }
             }
         } else {
@@ -451,19 +457,38 @@ __global__ __launch_bounds__(64 * W) void beam_rows_kernel(Shape sh, const T* lo
         n = 0;
         ++joins;
     }
+    // The sum beside the largest logit, of the whole stretch: over its term as this wave
+    // makes terms, so that what the one logit leaves of the sum is 1.  Another wave may
+    // hold one that this wave's terms cannot express.
     sum = all_sum(sum);
-    if (lane == 0) {
-        tops[wave] = (double)base + (kMagic - shift) * kLn2;
-        sums[wave] = sum;
+    const uint64_t first = list[0];
+    const float most = first ? image_value((uint32_t)(first >> 32)) : -FLT_MAX;
+    if (!first) {
+        sum = 0.0;
+    } else if (!(most <= (TABLE && by_table ? 63.75f : c + 600.0f))) {
+        sum *= exp64((double)base + (kMagic - shift) * kLn2 - (double)most);
+    } else if (TABLE && by_table) {
+        if constexpr (TABLE) {
+            u16x2 place;
+            const u16x2 at2 = ExpTable::offsets(__float_as_uint(most) >> 16, place);
+            double e = *reinterpret_cast<const double*>(reinterpret_cast<const char*>(table) + at2[0]);
+            if (place[0] == 0) e += ExpTable::rest((double)most);
+            sum /= e;
+        }
+    } else {
+        const double d = (double)max_number(most - base, c - base - 700.0f);
+        const double m[1] = {fma(d, kLog2e, shift)}, r[1] = {fma(m[0] - shift, -kLn2, d)};
+        double e[1];
+        exp_scaled(r, m, e);
+        sum /= e[0];
     }
+    if (lane == 0) sums[wave] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-        double m = tops[0], all = 0.0;
+        double all = 0.0;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) m = fmax(m, tops[w]);
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) all += sums[w] * exp64(tops[w] - m);
-        stats[blockIdx.x] = {m, all};
+        for (int w = 0; w < kWaves; ++w) all += sums[w];
+        stats[blockIdx.x] = {(double)most, all};
     }
     if (wave == 0 && lane < sh.n_out) keys[(int64_t)blockIdx.x * sh.n_out + lane] = list[lane];
 }

@@ -192,11 +192,12 @@ gdn_status gdn_slot_reorder(gdn_pool* pool, int32_t n_req, int32_t width, const 
  *                 matches no token; finished must then be NULL)
  *   workspace     device, >= gdn_beam_select_workspace_bytes, 256-byte aligned
  * Sorted by falling score; of equal scores the lower beam comes first, then the
- * larger logit, then the lower token.  Sums and scores are held in 64 bits; of
- * different beams, scores closer than 2^-40 of their size count as equal.  With
- * fewer continuations than n_out the rest gets parent and token -1, score
- * -infinity, finished 0.  No two of the outputs may overlap, nor an output an
- * input. */
+ * larger logit, then the lower token.  Sums and scores are held in 64 bits, with
+ * the largest logit's term exactly 1: a beam's only token keeps the beam's score,
+ * and no token raises it.  Of different beams, scores closer than 2^-40 of their
+ * size count as equal.  With fewer continuations than n_out the rest gets parent
+ * and token -1, score -infinity, finished 0.  No two of the outputs may overlap,
+ * nor an output an input. */
 gdn_status gdn_beam_select_workspace_bytes(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out,
                                            size_t* bytes);
 gdn_status gdn_beam_select(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype,
