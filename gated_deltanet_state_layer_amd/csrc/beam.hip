@@ -45,7 +45,7 @@ constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: a sum's low bits 
 // exp(r) 2^n of N values side by side, |r| <= ln 2 / 2 or a little more, n in the low
 // bits of m.  The polynomial is 1 + r + r^2 q(r), q the Chebyshev interpolation of
 // degree 8 (1.2e-15, what fp64 rounds), so that exp(0) is 1.  Degrees 8 and 9 in all
-// leave 2e-12 and 7e-14, where scores below 1 are told apart by 2^-40 of themselves.
+// leave 2e-12 and 7e-14, where scores below 1 are told apart by 2^-41 of themselves.
 // The barriers keep the N chains of dependent products interleaved.
 template <int N>
 __device__ __forceinline__ void exp_scaled(const double (&r)[N], const double (&m)[N], double (&p)[N]) {
@@ -97,11 +97,16 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t token) {
     return x > kNone ? (uint64_t)image(fminf(x, FLT_MAX)) << 32 | (uint32_t)~token : 0;
 }
 
-// A continuation: its score's image to 52 bits, then beam * 64 + place in the beam's
-// list, the lower the better: scores within 2^-40 of their size count as equal.
-// 0: none.
+// A continuation: the image of its score, rounded to 41 bits, then beam * 64 + place in
+// the beam's list, the lower the better: scores that are equal in 41 bits are equal.
+// Rounded to nearest, since scores are often numbers of 24 bits (a beam's own, with
+// one token left): they lie in the middle of what is rounded to them.  0: none.
 __device__ __forceinline__ uint64_t entry_of(double score, uint32_t tag) {
-    return (image(score) & ~(uint64_t)0xfff) | (0xfff - tag);
+    const uint64_t u = (__builtin_bit_cast(uint64_t, score) + 0x800) & ~(uint64_t)0xfff;
+    return (image(__builtin_bit_cast(double, u)) & ~(uint64_t)0xfff) | (0xfff - tag);
+}
+__device__ __forceinline__ double entry_score(uint64_t e) {
+    return __builtin_bit_cast(double, e >> 63 ? (e & ~(uint64_t)0xfff) ^ (uint64_t)1 << 63 : ~(e | 0xfff));
 }
 
 // The value of lane (this ^ MASK).  Inside rows of 16 lanes by DPP, across them by the
@@ -502,8 +507,6 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
                                                                   uint8_t* finished_out) {
     __shared__ uint64_t held[kMergeWaves][128];
     __shared__ int32_t token[GDN_BEAM_MAX * GDN_BEAM_MAX];
-    __shared__ float logit[GDN_BEAM_MAX * GDN_BEAM_MAX];
-    __shared__ double norms[GDN_BEAM_MAX][2];
     auto* lists = reinterpret_cast<uint64_t(*)[64]>(held);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t req = blockIdx.x;
@@ -524,12 +527,10 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
         if (!(fabsf(base) <= FLT_MAX)) continue;
         const uint32_t tag = b * 64 + lane;
         uint64_t e = 0;
-        if (done) {   // as a logit of 0 with nothing to subtract
+        if (done) {
             if (lane == 0) {
                 e = entry_of((double)base, tag);
                 token[tag] = eos;
-                logit[tag] = 0.0f;
-                norms[b][0] = norms[b][1] = 0.0;
             }
         } else {
             const double c = all_max(st.c);
@@ -569,13 +570,8 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
             }
             if (n > 0) join();
             if (best && lane < sh.n_out) {
-                logit[tag] = image_value((uint32_t)(best >> 32));
                 token[tag] = (int32_t)~(uint32_t)best;
-                e = entry_of((double)base + (((double)logit[tag] - c) - norm), tag);
-            }
-            if (lane == 0) {
-                norms[b][0] = c;
-                norms[b][1] = norm;
+                e = entry_of((double)base + (((double)image_value((uint32_t)(best >> 32)) - c) - norm), tag);
             }
         }
         mine = b < kMergeWaves ? e : merge64(mine, e);
@@ -589,9 +585,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, con
     const int parent = some ? tag / 64 : -1, tok = some ? token[tag] : -1;
     parents[at] = parent;
     tokens[at] = tok;
-    scores_out[at] = some ? (float)((double)scores[req * sh.width + parent] +
-                                    (((double)logit[tag] - norms[parent][0]) - norms[parent][1]))
-                          : kNone;
+    scores_out[at] = some ? (float)entry_score(mine) : kNone;   // of the rounded score: it never rises
     if (finished_out)
         finished_out[at] = some && ((finished && finished[req * sh.width + parent]) || tok == eos);
 }

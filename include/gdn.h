@@ -186,7 +186,7 @@ gdn_status gdn_slot_reorder(gdn_pool* pool, int32_t n_req, int32_t width, const 
  *                 byte has one continuation, the token eos at its own score
  *   parents       device int32 [n_req][n_out]: the beam continued
  *   tokens        device int32 [n_req][n_out]
- *   scores_out    device fp32 [n_req][n_out], rounded once
+ *   scores_out    device fp32 [n_req][n_out]
  *   finished_out  device bytes [n_req][n_out], or NULL: 1 where the beam
  *                 continued was finished or the token is eos (a negative eos
  *                 matches no token; finished must then be NULL)
@@ -194,10 +194,10 @@ gdn_status gdn_slot_reorder(gdn_pool* pool, int32_t n_req, int32_t width, const 
  * Sorted by falling score; of equal scores the lower beam comes first, then the
  * larger logit, then the lower token.  Sums and scores are held in 64 bits, with
  * the largest logit's term exactly 1: a beam's only token keeps the beam's score,
- * and no token raises it.  Of different beams, scores closer than 2^-40 of their
- * size count as equal.  With fewer continuations than n_out the rest gets parent
- * and token -1, score -infinity, finished 0.  No two of the outputs may overlap,
- * nor an output an input. */
+ * and no token raises it.  Scores are rounded to 41 significant bits, compared as
+ * such, and rounded to fp32 from there.  With fewer continuations than n_out the
+ * rest gets parent and token -1, score -infinity, finished 0.  No two of the
+ * outputs may overlap, nor an output an input. */
 gdn_status gdn_beam_select_workspace_bytes(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out,
                                            size_t* bytes);
 gdn_status gdn_beam_select(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype,

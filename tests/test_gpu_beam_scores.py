@@ -1,8 +1,8 @@
 """GPU: beam selection where scores of different beams are equal or nearly so, and
 rows whose distribution is (almost) certain: the order, and scores to their rounding.
 
-Scores are sums in 64 bits.  What is exact on the host here is exact by arithmetic: a
-row with one token left adds 0 to its beam."""
+Scores are sums in 64 bits, rounded to 41 before they are compared.  What is exact on
+the host here is exact by arithmetic: a row with one token left adds 0 to its beam."""
 import math
 
 import pytest
@@ -95,3 +95,77 @@ def test_nearly_certain_rows(G, r, w, v, dtype):
         # rounded to fp32; a sum of v terms above 1 in fp64, each addition half a step
         lim = ref.abs() * (2.0 ** -24 + 2.0 ** -40) + v * 2.0 ** -53
         assert ((got - ref).abs() <= lim).all(), float(((got - ref).abs() / lim).max())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("r,w,v", SIZES)
+def test_shifted_rows_are_equal(G, r, w, v, dtype):
+    """Rows that differ by a constant have equal distributions.  Logits are eighths
+    below 32, exact in either type, so the definition gives equal scores; where that
+    score is nearer than 2^-47 of itself (64 times what fp64 sums leave) to the border
+    between two numbers of 41 bits, the request does not count."""
+    g = torch.Generator().manual_seed(v + 3)
+    levels = torch.randint(-96, 97, (r, 1, v), generator=g)
+    levels[:, :, :8] = torch.arange(97, 105)   # the best ones, all different
+    shift = 8 * torch.randint(-17, 18, (r, w, 1), generator=g)
+    x = ((levels + shift) / 8.0).to(dtype)
+    assert torch.equal(x.double() * 8, (levels + shift).double())
+    row = levels[:, 0].double() / 8
+    base = -8 * torch.rand(r, 1, generator=g).double()
+    base = base.float().double()
+    score = base + (row[:, :8] - row.amax(1, keepdim=True)) - torch.log(
+        torch.exp(row - row.amax(1, keepdim=True)).sum(1, keepdim=True))
+    frac, _ = torch.frexp(score.abs())
+    border = ((frac * 2.0 ** 41 % 1.0) - 0.5).abs() * 2.0 ** -41 / frac
+    clear = (border >= 2.0 ** -47).all(1)
+    assert clear.float().mean() > 0.5
+    k = min(64, 8 * w)
+    parents, tokens, out = _select(G, x.cuda(), base.float().expand(r, w).contiguous(), k)
+    assert torch.equal(parents[clear], (torch.arange(k) % w).int().expand(r, k)[clear])
+    assert torch.equal(tokens[clear], (7 - torch.arange(k) // w).int().expand(r, k)[clear])
+    assert torch.equal(out[clear][:, ::w], out[clear][:, w - 1::w])
+    ref = score.flip(1)[:, torch.arange(k) // w]
+    assert ((out.double() - ref).abs() <= ref.abs() * (2.0 ** -24 + 2.0 ** -40) + v * 2.0 ** -53).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("r,w,v", SIZES)
+def test_scores_equal_in_41_bits(G, r, w, v, dtype):
+    """Every other beam has a second token that takes 2^-44.7 of the probability:
+    in 41 bits that leaves the beam's score, a number of 24, as it was."""
+    g = torch.Generator().manual_seed(v + 4)
+    x = torch.full((r, w, v), NONE, dtype=dtype, device="cuda")
+    best = torch.randint(0, 9, (r, w, 1), generator=g) / 4.0
+    at = torch.randint(0, v // 2, (r, w, 1), generator=g)
+    x.scatter_(2, at.cuda(), best.to(dtype).cuda())
+    second = torch.where(torch.arange(w)[None, :, None] % 2 == 0, best - 31.0, NONE)
+    assert torch.equal(second, second.to(dtype).float())
+    x.scatter_(2, v // 2 + at.cuda(), second.to(dtype).cuda())
+    scores = (16 * torch.rand(r, 1, generator=g) - 8).expand(r, w).contiguous()
+    scores = torch.where(scores.abs() < 0.25, 1.0, scores)     # from 0.25 on, half a step of 41 bits is 2^-43 or more
+    parents, tokens, out = _select(G, x, scores, w)
+    assert (parents == torch.arange(w)).all() and torch.equal(tokens, at[..., 0].int())
+    assert torch.equal(out, scores)
+
+
+@pytest.mark.parametrize("base", [-8.123, -0.3, -100.0])
+def test_scores_fall_where_they_lie_close(G, base):
+    """64 beams whose scores lie around a border between two fp32 numbers, closer than
+    2^-40 of their size: what comes out never rises."""
+    base = float(torch.tensor(base))
+    up = abs(base) * 2.0 ** -22
+    for seed in range(8):
+        g = torch.Generator().manual_seed(seed)
+        # the second token takes a fraction of about `up` of the sum; neighbouring fp32 logits
+        # change it by 1e-6 of that
+        lead = math.log(1 / up)
+        second = torch.full((64,), -lead)
+        for i in range(1, 64):
+            second[i] = torch.nextafter(second[i - 1], torch.tensor(-math.inf if seed % 2 else math.inf))
+        second = second[torch.randperm(64, generator=g)] if seed > 3 else second
+        x = torch.stack((torch.zeros(64), second), 1)[None]
+        parents, _, out = _select(G, x.cuda(), torch.full((1, 64), base), 64)
+        assert (out[:, :-1] >= out[:, 1:]).all(), seed
+        exact = (base - torch.log1p(torch.exp(second.double())))[parents[0].long()]
+        # 41 bits: half a step each, and what fp64 leaves
+        assert (exact[:-1] - exact[1:] >= -abs(base) * (2.0 ** -40 + 2.0 ** -50)).all(), seed
