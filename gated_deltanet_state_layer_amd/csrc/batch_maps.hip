@@ -90,9 +90,11 @@ __global__ __launch_bounds__(kThreads) void batch_maps_kernel(Maps a) {
     // this thread's first checkpoint row, in case it is one
     const uint32_t row0 = blockIdx.x * kThreads + tid;
     const int32_t slot0 = a.ckpt_every > 0 && row0 < min((uint32_t)a.n_free, most) ? a.free_slots[row0] : -1;
-    for (int c0 = 0; c0 < a.n_seq; c0 += kChunk) {
-        const int here = min(kChunk, a.n_seq - c0);
-        const bool writer = (unsigned)(c0 / kChunk) % gridDim.x == blockIdx.x;
+    // the last chunk may end at 2^31: what is left is counted down beside its start
+    uint32_t c0 = 0;
+    for (int left = a.n_seq; left > 0; left -= kChunk, c0 += kChunk) {
+        const int here = min(kChunk, left);
+        const bool writer = c0 / kChunk % gridDim.x == blockIdx.x;
         int32_t raw[PER];
 #pragma unroll
         for (int k = 0; k < PER; ++k) {   // neighbouring requests in neighbouring lanes
@@ -189,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void batch_maps_kernel(Maps a) {
                     if (t < lo || t >= hi) continue;
                     in |= 1u << i;
                     while (cu[j + 1] <= (uint32_t)t) ++j;   // ends: t < cu[kChunk]
-                    seq[i] = c0 + j;
+                    seq[i] = (int)c0 + j;
                     if (a.token_pos) pos[i] = past[j] + (int)((uint32_t)t - cu[j]);
                     if (a.token_adapter) ad[i] = adapter[j];
                 }
@@ -198,7 +200,7 @@ __global__ __launch_bounds__(kThreads) void batch_maps_kernel(Maps a) {
                 put4(a.token_adapter, (int64_t)r, ad, in, a.vec);
             }
         }
-        if (c0 + kChunk < a.n_seq) __syncthreads();   // cu[] is read out
+        if (left > kChunk) __syncthreads();   // cu[] is read out
     }
     if (carry > a.max_tok) bad |= kErrSeqlens;
     const uint32_t total = min(carry, a.max_tok);
