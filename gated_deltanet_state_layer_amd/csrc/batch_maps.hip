@@ -5,8 +5,8 @@
 // trips, so it is one launch without scratch memory.  Every workgroup loads what the
 // requests bring, all loads in one trip, scans the lengths itself (512 to 4096 at a
 // time, in LDS) and then fills its own rows; no workgroup waits for another.  All
-// maps of 64 requests 4.1 us (5.3 with the loads one behind the other and scans
-// through LDS), of 2000 requests with 300001 tokens 6.2 (3.6 MB).
+// maps of 64 requests 4.2 us (5.3 with the loads one behind the other and scans
+// through LDS), of 2000 requests with 300001 tokens and checkpoints 6.8 (3.7 MB).
 #include <algorithm>
 
 #include "gdn_common.h"
@@ -75,8 +75,8 @@ __device__ __forceinline__ void put4(int32_t* p, int64_t r, const int (&v)[kRows
 }
 
 // PER requests to a thread: as few as hold them all, since what the threads scan and
-// put into LDS grows with it (64 requests 4.1 us, eight to a thread 5.4; 2000 requests
-// four to a thread 6.2, eight 6.9).
+// put into LDS grows with it (64 requests 4.2 us, eight to a thread 5.6; 2000 requests
+// four to a thread 6.8, eight 8.1).
 template <int PER>
 __global__ __launch_bounds__(kThreads) void batch_maps_kernel(Maps a) {
     constexpr int kChunk = kThreads * PER;

@@ -15,10 +15,13 @@
 // whole numbers, right or wrong.  So exponentials and sums are fp64 here: the vector
 // units run them at fp32's rate.
 //
-// What bounds it is issuing these instructions, not memory: 64 x 8 x 131072 bf16
-// (134 MB) take 59 us (2.3 TB/s), 45 without exponentials, 37 without the selection,
-// about as much when the logits lie in the L2 caches.  In fp32 (268 MB) 76 us, 3.5
-// TB/s.  1 x 4 x 32000: 9.3 us, of which two launches are 3.8.
+// 64 x 8 x 131072 bf16 (134 MB) take 58 us (2.3 TB/s), 47 without exponentials, 43
+// without the selection, about as much when the logits lie in the L2 caches.  No unit
+// is busy all the time: the vector units issue in 40 % of the cycles, LDS works in 20 %,
+// and waves wait for 61 % of theirs.  What bounds it is latency at four waves to a SIMD,
+// as many as 76 KB of LDS a workgroup (half of it the table, half the keys that wait)
+// leave room for, with a barrier in each step.  In fp32 (268 MB) 73 us, 3.7 TB/s.
+// 1 x 4 x 32000: 9.5 us, of which two launches are 3.8.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -263,8 +266,8 @@ __device__ __forceinline__ float max_number(float a, float b) {
 // exp of bf16 values by table: those of magnitudes 2^-13 up to 64, both signs, an
 // entry of 1 for what is smaller (with a correction where it is not 0), and of 0 for
 // what is larger (negative, and far below the row's largest: see where it is used).
-// Looking one up takes a quarter of the vector instructions of computing one (26.3
-// to 16.4 million in all at 64 x 8 x 131072), and an LDS read whose lanes' places
+// Looking one up takes a quarter of the vector instructions of computing one (26.0
+// to 16.0 million in all at 64 x 8 x 131072), and an LDS read whose lanes' places
 // collide (4.5 of 8.2 million LDS cycles are conflicts).
 struct ExpTable {
     static constexpr int kFirst = 0x3900, kPast = 0x4280, kSize = kPast - kFirst + 2;   // bits of 2^-13 and 64
@@ -499,7 +502,7 @@ __global__ __launch_bounds__(64 * W) void beam_rows_kernel(Shape sh, const T* lo
 }
 
 // One workgroup per request: each wave puts the stretches of its beams together, then
-// half of the waves' lists go into the other half's at a time.  4.7 us for 64 x 8
+// half of the waves' lists go into the other half's at a time.  4.9 us for 64 x 8
 // beams, a launch and three trips to memory.
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(Shape sh, const Stretch* stats, const uint64_t* keys,
                                                                   const float* scores, const uint8_t* finished, int eos,
@@ -600,9 +603,9 @@ Shape beam_shape(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, int
 
 // Workgroups of eight waves with the table, two to a CU, where each has eight steps or
 // more to fill it for; of four waves otherwise, four to a CU.  With the table and
-// without it: 64 x 8 x 131072 59 and 73 us, 32 x 8 x 131072 38 and 44, 64 x 8 x 32000
-// (eight steps) 28.7 and 30.9, 64 x 4 x 32000 (four) 21.0 and 20.2, 1 x 4 x 32000 12.7
-// and 9.5.  Twice the workgroups with the table: 77 us for 64 x 8 x 131072.
+// without it: 64 x 8 x 131072 58 and 77 us, 32 x 8 x 131072 38 and 46, 64 x 8 x 32000
+// (eight steps) 28.0 and 31.0, 64 x 4 x 32000 (four) 20.7 and 20.0, 1 x 4 x 32000 11.7
+// and 9.5.  Twice the workgroups with the table: 68 us for 64 x 8 x 131072.
 Shape beam_plan(int32_t n_req, int32_t width, int32_t vocab, int32_t n_out, gdn_dtype dtype) {
     const Shape s = beam_shape(n_req, width, vocab, n_out, 8, 512);
     return dtype == GDN_BF16 && s.steps >= 8 ? s : beam_shape(n_req, width, vocab, n_out, 4, 1024);

@@ -42,9 +42,12 @@ inline bool mx_proj_fits(int64_t n_tok, int64_t n_out) {
 // per 1024 inputs; of tiles about 4 us and, per 1024 inputs, 8.8 (128x128) or
 // 12.2 (128x192).  Fitted to 19 token counts of 24 to 8192 for each of eleven
 // pairs of 128 to 8192 inputs and 1001 to 16384 channels: what is picked takes
-// 0.5 % longer than the fastest of these on average, 17 % at worst.  The 64-token
-// shape is no part of it: tiles add in another order, and a call keeps its bits
-// (128 x 2048 -> 12352 takes tiles, 26.6 us, and would take 18.7 in that shape).
+// 0.5 % longer than the fastest of these on average, 17 % at worst.  The skinny
+// kernel's shape of 64 tokens is no part of the fit, and where it saves rounds tiles
+// are taken that are slower than it (128 x 2048 -> 12352 26.6 us, in that shape 18.7):
+// such calls give the last bits that tiles give, which add in another order.  Nor are
+// adapters, of which a tile multiplies all that its tokens have, one after the other
+// (2048 -> 12352 at rank 16 with one each: 96 tokens, skinny, 32 us; 128, tiles, 115).
 inline int64_t mx_skinny_time(int64_t n_tok, int32_t n_in, int64_t n_out) {
     return mx_rounds(mx_tiles(n_tok, n_out, 32, 64)) * (2560 + (int64_t)n_in * 8 / 5);
 }

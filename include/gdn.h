@@ -165,10 +165,12 @@ gdn_status gdn_slot_copy(gdn_pool* pool, int32_t n, const int32_t* src_ids, cons
  * slots_out[r] is a permutation of slots[r].  The first child of a beam keeps
  * its slot; every other beam takes, in increasing order, the slot of a beam
  * without children, in increasing order.  Only these are copied (none for a beam
- * without a parent, whose slot keeps what it held).  slots_out may be slots;
- * otherwise the two must not overlap.  Slots must be distinct within a call
- * (GDN_VALIDATE rejects repeated slots and slots >= n_slots); a copy that would
- * touch a slot >= n_slots is skipped and sets the sticky error word. */
+ * without a parent, whose slot keeps what it held).  A beam that gets a negative
+ * id has no state: padding beams should come last, and no more beams have a parent
+ * than have a slot.  slots_out may be slots; otherwise the two must not overlap.
+ * Slots must be distinct within a call (GDN_VALIDATE rejects repeated slots and
+ * slots >= n_slots); a copy that would touch a slot >= n_slots is skipped and sets
+ * the sticky error word. */
 #define GDN_BEAM_MAX 64
 gdn_status gdn_slot_reorder(gdn_pool* pool, int32_t n_req, int32_t width, const int32_t* slots,
                             const int32_t* parents, int32_t* slots_out, void* stream);
